@@ -19,6 +19,11 @@
  *   cache    -> ft_slot_*         host LRU of expert slots in a device pool
  *   EP       -> ft_ep_plan, ft_gather_rows   experts split over ranks; the rows
  *                                 of each rank's experts exchanged all-to-all
+ *   FP8      -> ft_fp8_quant_rows, ft_fp8_pack, ft_fp8_gemm, ft_moe_ffn_fp8   E4M3 codes
+ *                                 with an fp32 scale per block of 128: the product
+ *                                 and the expert FFN over FP8 slots
+ *   router   -> ft_moe_balance, ft_moe_route_backward   per-expert counts and balance
+ *                                 loss; the gradient of the router's logits
  *
  * Conventions (all functions):
  *   - Return an int status (FT_OK or a negative FT_ERR_*).  On FT_ERR_CUDA the
@@ -99,7 +104,7 @@ typedef struct {
   int64_t global_off[3];
   int64_t slot_bytes;
   int32_t num_slots;      /* slots in the pool the layout describes */
-  int32_t scale_format;   /* FT_SCALE_NVFP4 or FT_SCALE_MXFP4 */
+  int32_t scale_format;   /* FT_SCALE_NVFP4, FT_SCALE_MXFP4 or FT_SCALE_FP8 */
   int32_t tiled;          /* 0: codes [N, K/2] and scales [N, ld_scale] row-major;
                              1: stage-tiled (see ft_tiled_slot_layout_init) */
 } ft_nvfp4_slot_layout;
@@ -114,7 +119,10 @@ typedef struct {
  *                   the dequantised values and multiply back in fp32 (the
  *                   values are e2m1 * 2^(s - 127), the global only keeps the
  *                   f16 dequantisation exact). */
-enum { FT_SCALE_NVFP4 = 0, FT_SCALE_MXFP4 = 1 };
+enum { FT_SCALE_NVFP4 = 0, FT_SCALE_MXFP4 = 1, FT_SCALE_FP8 = 2 /* see ft_fp8_slot_layout_init */ };
+
+/* Element types of float buffers, where a call takes more than one. */
+enum { FT_F32 = 0, FT_BF16 = 1, FT_F16 = 2 };
 
 /* Fill *out with the canonical layout for hidden size H, intermediate I and
  * num_slots slots.  H and I must be multiples of 64.  Returns FT_OK or
@@ -136,11 +144,27 @@ FT_API int ft_tiled_slot_layout_init(int H, int I, int num_slots, int scale_form
                                      ft_nvfp4_slot_layout* out);
 
 /*
+ * The slot layout of FP8 experts (scale_format = FT_SCALE_FP8, row-major).
+ * For a tensor [N, K]:
+ *   codes   uint8 [N, K]                      one E4M3 (FN) code per value
+ *   scales  fp32 [ceil(N/128), ld_scale / 4]  one scale per 128 x 128 block
+ * value(n, k) = e4m3(code) * scale[n / 128][k / 128].  ld_scale is the bytes
+ * of a scale row, 4 ceil(K/128) rounded up to 16; the padding scales are
+ * zero and the three globals are not used.  H and I must be multiples of 64
+ * (the last block of a row or column may be half a block).  The slot manager
+ * takes the layout as it takes the others; ft_moe_ffn_fp8 reads it.
+ * Pages: FP8 stands beside MXFP4, NVFP4 and BF16 among the expert formats
+ * (About page, "Broad MoE & Ecosystem Support"); no page defines its scales,
+ * so the 128 x 128 block is this library's reading.
+ */
+FT_API int ft_fp8_slot_layout_init(int H, int I, int num_slots, ft_nvfp4_slot_layout* out);
+
+/*
  * Pack fp32 weights w [N, K] (device; N, K the shape of tensor `mat` of the
  * layout) into the tensor's place in one slot (slot: device address of the
  * slot's first byte), in the layout's scale format and arrangement: the
  * arithmetic of ft_nvfp4_pack or ft_mxfp4_pack, the bytes placed as the
- * layout says.  ws as for those calls.
+ * layout says (ft_fp8_pack for an FP8 layout).  ws as for those calls.
  */
 FT_API int ft_pack_slot(const float* w, int mat, const ft_nvfp4_slot_layout* layout, void* slot, void* ws,
                         ft_stream_t stream);
@@ -363,6 +387,125 @@ FT_API int ft_nvfp4_pack(const float* w, int N, int K, uint8_t* codes, uint8_t* 
 FT_API int ft_mxfp4_pack(const float* w, int N, int K, uint8_t* codes, uint8_t* scales, int ld_scale,
                   float* global_scale, void* ws, ft_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * FP8: E4M3 codes with one fp32 scale per block of 128, 1 x 128 along a row for
+ * activations and 128 x 128 for weights.  Of a block with values x_i:
+ *   m   = max(max |x_i|, 2^-100)           (NaN left out of the maximum)
+ *   s   = m / 448                          (fp32, the stored scale)
+ *   q_i = E4M3_rne_sat((448 x_i) / m)      (fp32 product, then fp32 division)
+ * and the value of a code is e4m3(q_i) * s.  Ties go to the even code; for
+ * bf16 and f16 inputs 448 x_i is exact, so the ties are those of the exact
+ * quotient.  A NaN becomes the code 0x7F (NaN); an infinity makes the scale
+ * infinite, so that the whole block reads as NaN.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Rows of activations to FP8.
+ *   x       device [M, K] of type x_type (FT_F32, FT_BF16, FT_F16), row pitch ld_x elements
+ *   codes   device uint8 [M, K] (out), row pitch ld_codes bytes, a multiple of 16; 16-byte aligned
+ *   scales  device fp32 [M, ceil(K/128)] (out), row pitch ld_scales elements
+ * Bytes past K of a code row and scales past ceil(K/128) are not written.
+ * M = 0 is a no-op.  M * ceil(K/128) < 2^31.
+ */
+FT_API int ft_fp8_quant_rows(const void* x, int x_type, int M, int K, int64_t ld_x, uint8_t* codes,
+                             int64_t ld_codes, float* scales, int64_t ld_scales, ft_stream_t stream);
+
+/*
+ * An fp32 weight [N, K] (device, contiguous) to FP8 in 128 x 128 blocks.
+ *   codes   device uint8 [N, K] (out), row pitch ld_codes bytes, a multiple of 16; 16-byte aligned
+ *   scales  device fp32 [ceil(N/128), ld_scales] (out; columns past ceil(K/128) zeroed)
+ */
+FT_API int ft_fp8_pack(const float* w, int N, int K, uint8_t* codes, int64_t ld_codes, float* scales,
+                       int ld_scales, ft_stream_t stream);
+
+/*
+ * The product of FP8 rows with an FP8 weight:
+ *   out[m, n] = sum_b sa[m, b] sb[n / 128, b] sum_{k in block b} e4m3(a[m, k]) e4m3(b[n, k])
+ * with the sums in fp32 and one rounding to the output's type.
+ *   a, b      device uint8 [M, K], [N, K]; row pitches lda, ldb bytes, multiples of 16; 16-byte aligned
+ *   sa        device fp32 [M, ceil(K/128)], row pitch ld_sa elements
+ *   sb        device fp32 [ceil(N/128), ceil(K/128)], row pitch ld_sb elements
+ *   out       device [M, N] of type out_type (FT_F32 or FT_BF16), row pitch ldo elements (out)
+ *   ws        device workspace of ft_fp8_gemm_workspace_size bytes, 256-byte aligned; no zeroing
+ * Any M, N, K from 1 up (K < 2^24); no alignment of M, N or K is needed.  M = 0 is a no-op.
+ */
+FT_API int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64_t ld_sa, const uint8_t* b,
+                       int64_t ldb, const float* sb, int64_t ld_sb, int M, int N, int K, void* out, int out_type,
+                       int64_t ldo, void* ws, size_t ws_bytes, ft_stream_t stream);
+FT_API size_t ft_fp8_gemm_workspace_size(int M, int N, int K);
+
+/*
+ * ft_moe_ffn_nvfp4 over FP8 experts.  For row r of group e (token
+ * t = perm_src[r] / k):
+ *   (cx, sx)    = FP8 of x_t                       (as ft_fp8_quant_rows)
+ *   G, U        = gate and up products of (cx, sx) (as ft_fp8_gemm, fp32)
+ *   h           = G / (1 + e^-G) * U               (fp32)
+ *   (ch, sh)    = FP8 of h, per 128 of I
+ *   out_perm[r] = down product of (ch, sh)         (fp32 sums, rounded once to out_type)
+ * Arguments as for ft_moe_ffn_nvfp4, with an FP8 layout; out_perm is device
+ * [T*k, H] of type out_type (FT_F32, or FT_BF16: half the bytes, read by
+ * ft_moe_combine_bf16); ws holds ft_moe_ffn_fp8_workspace_size bytes, 256-byte
+ * aligned, and needs no zeroing.  A non-empty group whose slot is -1 sets
+ * FT_DEV_NOT_RESIDENT and its rows are left unwritten, as are rows behind
+ * expert_offsets[E]; a slot or a token out of range sets FT_DEV_BAD_INDEX (the
+ * rows of that slot are left unwritten, a row of that token reads as zeros).
+ * Non-finite values follow the formulas above.
+ */
+FT_API int ft_moe_ffn_fp8(const void* x, int T, int H, int I, int E, int k, const int32_t* perm_src,
+                          const int32_t* expert_offsets, const int32_t* slot_table, const void* slot_pool,
+                          const ft_nvfp4_slot_layout* layout, void* out_perm, int out_type, void* ws,
+                          size_t ws_bytes, ft_stream_t stream);
+FT_API size_t ft_moe_ffn_fp8_workspace_size(int T, int H, int I, int E, int k);
+
+/* ft_moe_combine over bf16 expert outputs (out_perm device bf16 [T*k, H]): the
+ * same fp32 sum in the same order, y fp32 [T, H].  H % 8 == 0; out_perm and y
+ * 16-byte aligned. */
+FT_API int ft_moe_combine_bf16(const void* out_perm, const int32_t* pair_to_row, const float* topk_w, int T, int k,
+                               int H, void* y, ft_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * How evenly a router spreads its tokens, and the gradient of its logits.
+ * Over the Tv tokens with valid[t] != 0 (all T when valid is NULL), with
+ * p[t] = softmax(logits[t]) over all E experts:
+ *   counts[e] = number of (t, j) with topk_ids[t, j] = e
+ *   loss      = coef * E / (Tv k) * sum_e counts[e] * (1 / Tv) sum_t p[t, e]     (0 when Tv = 0)
+ * which is coef when the tokens and the probabilities are spread evenly.
+ * ------------------------------------------------------------------------- */
+
+/*
+ *   logits    device fp32 [T, E], row pitch ld elements
+ *   topk_ids  device int32 [T, k] (from ft_moe_route; those of tokens that are not valid are not read)
+ *   valid     device uint8 [T], or NULL
+ *   counts    device int32 [E] (out), n_valid device int32 [1] (out): Tv, loss device fp32 [1] (out)
+ *   ws        device workspace of ft_moe_balance_workspace_size bytes, 16-byte aligned; no zeroing
+ * Requires 1 <= k <= min(E, 32), E <= 1024.  An id outside [0, E) sets
+ * FT_DEV_BAD_INDEX and is not counted; an id that a token repeats counts each time.
+ * A row whose logits are all -inf has no probabilities (p = 0).  Deterministic.
+ * T = 0 writes zeros.
+ */
+FT_API int ft_moe_balance(const float* logits, int64_t ld, const int32_t* topk_ids, const uint8_t* valid, int T, int E,
+                          int k, float coef, int32_t* counts, int32_t* n_valid, float* loss, void* ws, size_t ws_bytes,
+                          ft_stream_t stream);
+FT_API size_t ft_moe_balance_workspace_size(int T, int E);
+
+/*
+ * dlogits (written, not added to) of the balance loss and of the router's weights, in one pass:
+ *   dlogits[t, e]     = dloss * coef * E / (Tv^2 k) * p[t, e] (counts[e] - sum_i p[t, i] counts[i])
+ *   dlogits[t, id_j] += w_j (dw_j - sum_i w_i dw_i)
+ * counts are constants of the loss, as the choice of the experts has no gradient.  Rows of tokens that
+ * are not valid are zero.
+ *   counts, n_valid   from ft_moe_balance; counts NULL leaves the first line out (logits may be NULL then)
+ *   dloss             device fp32 [1], or NULL for 1
+ *   topk_w, dw        device fp32 [T, k]; dw NULL leaves the second line out (topk_w may be NULL then)
+ *   topk_ids          device int32 [T, k] (read for the second line); one outside [0, E) sets FT_DEV_BAD_INDEX
+ *   dlogits           device fp32 [T, E], row pitch ldd elements (out)
+ * w is the softmax of the selected logits in both modes of ft_moe_route, so one gradient serves both.
+ */
+FT_API int ft_moe_route_backward(const float* logits, int64_t ld, const int32_t* topk_ids, const float* topk_w,
+                                 const float* dw, const uint8_t* valid, int T, int E, int k, float coef,
+                                 const int32_t* counts, const int32_t* n_valid, const float* dloss, float* dlogits,
+                                 int64_t ldd, ft_stream_t stream);
+
 /*
  * Read (and optionally clear) the per-device status word of the current
  * device.  Synchronises the device.  *status receives an FT_DEV_* code.
@@ -522,7 +665,13 @@ enum {
   FT_KERNEL_GATHER = 9,       /* row gather of the expert-parallel exchange */
   FT_KERNEL_ROUTE_PERMUTE = 10, /* route and permute in one launch (small batches) */
   FT_KERNEL_LAYER_DECODE = 11,  /* the whole layer in one launch (ft_moe_layer_nvfp4, small batches) */
-  FT_KERNEL_KINDS = 12,
+  FT_KERNEL_FP8_QUANT = 12,     /* rows to FP8 */
+  FT_KERNEL_FP8_GEMM = 13,      /* ft_fp8_gemm */
+  FT_KERNEL_FP8_GATE_UP = 14,   /* FP8 experts: grouped gate/up product + SwiGLU */
+  FT_KERNEL_FP8_DOWN = 15,      /* FP8 experts: grouped down product */
+  FT_KERNEL_BALANCE = 16,
+  FT_KERNEL_ROUTE_BACKWARD = 17,
+  FT_KERNEL_KINDS = 18,
 };
 
 typedef struct {

@@ -29,6 +29,7 @@ FT_DEV_F16_RANGE = 4
 FT_ROUTE_SOFTMAX_RENORM = 0
 FT_ROUTE_TOPK_SOFTMAX = 1
 FT_GATE, FT_UP, FT_DOWN = 0, 1, 2
+FT_F32, FT_BF16, FT_F16 = 0, 1, 2
 FT_SLOT_DEVICE = 0
 FT_SLOT_HOST_ONLY = 1
 
@@ -54,7 +55,8 @@ class SlotLayout(ctypes.Structure):
 
 
 FT_KERNEL_NAMES = ("route", "permute", "schedule", "gemm_gate_up", "gemm_down", "combine", "pack", "prep_x",
-                   "ffn_decode", "gather", "route_permute", "layer_decode")
+                   "ffn_decode", "gather", "route_permute", "layer_decode", "fp8_quant", "fp8_gemm", "fp8_gate_up",
+                   "fp8_down", "balance", "route_backward")
 
 
 class Profile(ctypes.Structure):
@@ -89,6 +91,22 @@ _SIGS = {
     "ft_moe_layer_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
     "ft_nvfp4_pack": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
     "ft_mxfp4_pack": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p]),
+    "ft_fp8_slot_layout_init": (c_int, [c_int, c_int, c_int, POINTER(SlotLayout)]),
+    "ft_fp8_quant_rows": (c_int, [c_void_p, c_int, c_int, c_int, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                  c_void_p]),
+    "ft_fp8_pack": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int64, c_void_p, c_int, c_void_p]),
+    "ft_fp8_gemm": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int, c_int,
+                            c_int, c_void_p, c_int, c_int64, c_void_p, c_size_t, c_void_p]),
+    "ft_fp8_gemm_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+    "ft_moe_ffn_fp8": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                               POINTER(SlotLayout), c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "ft_moe_ffn_fp8_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "ft_moe_combine_bf16": (c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p]),
+    "ft_moe_balance": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_int, c_int, c_int, c_float, c_void_p, c_void_p,
+                               c_void_p, c_void_p, c_size_t, c_void_p]),
+    "ft_moe_balance_workspace_size": (c_size_t, [c_int, c_int]),
+    "ft_moe_route_backward": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int,
+                                      c_float, c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
     "ft_device_status": (c_int, [POINTER(c_int), c_int]),
     "ft_device_status_detail": (c_int, [POINTER(c_int64)]),
     "ft_selftest_wait_timeout": (c_int, [c_void_p, c_void_p]),
@@ -130,13 +148,16 @@ def check(code: int) -> None:
         raise FtError(code, lib().ft_last_error().decode())
 
 
-FT_SCALE_NVFP4, FT_SCALE_MXFP4 = 0, 1
+FT_SCALE_NVFP4, FT_SCALE_MXFP4, FT_SCALE_FP8 = 0, 1, 2
 
 
 def slot_layout(H: int, I: int, num_slots: int, fmt: int = FT_SCALE_NVFP4, tiled: bool = False) -> SlotLayout:
     L = SlotLayout()
     if tiled:
         check(lib().ft_tiled_slot_layout_init(H, I, num_slots, fmt, ctypes.byref(L)))
+        return L
+    if fmt == FT_SCALE_FP8:
+        check(lib().ft_fp8_slot_layout_init(H, I, num_slots, ctypes.byref(L)))
         return L
     init = lib().ft_mxfp4_slot_layout_init if fmt == FT_SCALE_MXFP4 else lib().ft_nvfp4_slot_layout_init
     check(init(H, I, num_slots, ctypes.byref(L)))
@@ -217,6 +238,50 @@ def nvfp4_pack(w, N, K, codes, scales, ld_scale, global_scale, ws, stream) -> No
 
 def mxfp4_pack(w, N, K, codes, scales, ld_scale, global_scale, ws, stream) -> None:
     check(lib().ft_mxfp4_pack(w, N, K, codes, scales, ld_scale, global_scale, ws, stream))
+
+
+def fp8_quant_rows(x, x_type, M, K, ld_x, codes, ld_codes, scales, ld_scales, stream) -> None:
+    check(lib().ft_fp8_quant_rows(x, x_type, M, K, ld_x, codes, ld_codes, scales, ld_scales, stream))
+
+
+def fp8_pack(w, N, K, codes, ld_codes, scales, ld_scales, stream) -> None:
+    check(lib().ft_fp8_pack(w, N, K, codes, ld_codes, scales, ld_scales, stream))
+
+
+def fp8_gemm_workspace_size(M, N, K) -> int:
+    return int(lib().ft_fp8_gemm_workspace_size(M, N, K))
+
+
+def fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo, ws, ws_bytes, stream) -> None:
+    check(lib().ft_fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo, ws, ws_bytes, stream))
+
+
+def ffn_fp8_workspace_size(T, H, I, E, k) -> int:
+    return int(lib().ft_moe_ffn_fp8_workspace_size(T, H, I, E, k))
+
+
+def ffn_fp8(x, T, H, I, E, k, perm_src, offsets, slot_table, pool, layout, out_perm, out_type, ws, ws_bytes,
+            stream) -> None:
+    check(lib().ft_moe_ffn_fp8(x, T, H, I, E, k, perm_src, offsets, slot_table, pool, ctypes.byref(layout), out_perm,
+                               out_type, ws, ws_bytes, stream))
+
+
+def combine_bf16(out_perm, pair_to_row, w, T, k, H, y, stream) -> None:
+    check(lib().ft_moe_combine_bf16(out_perm, pair_to_row, w, T, k, H, y, stream))
+
+
+def balance_workspace_size(T, E) -> int:
+    return int(lib().ft_moe_balance_workspace_size(T, E))
+
+
+def balance(logits, ld, ids, valid, T, E, k, coef, counts, n_valid, loss, ws, ws_bytes, stream) -> None:
+    check(lib().ft_moe_balance(logits, ld, ids, valid, T, E, k, coef, counts, n_valid, loss, ws, ws_bytes, stream))
+
+
+def route_backward(logits, ld, ids, w, dw, valid, T, E, k, coef, counts, n_valid, dloss, dlogits, ldd,
+                   stream) -> None:
+    check(lib().ft_moe_route_backward(logits, ld, ids, w, dw, valid, T, E, k, coef, counts, n_valid, dloss, dlogits,
+                                      ldd, stream))
 
 
 def device_status(clear: bool = True) -> int:

@@ -61,6 +61,30 @@ extern "C" int ft_nvfp4_slot_layout_init(int H, int I, int num_slots, ft_nvfp4_s
   return FT_OK;
 }
 
+extern "C" int ft_fp8_slot_layout_init(int H, int I, int num_slots, ft_nvfp4_slot_layout* out) {
+  if (!out || H <= 0 || I <= 0 || H % 64 || I % 64 || num_slots <= 0)
+    return fail(FT_ERR_INVALID_ARG, "ft_fp8_slot_layout_init: need H, I multiples of 64 and num_slots > 0");
+  ft_nvfp4_slot_layout L{};
+  L.H = H;
+  L.I = I;
+  L.num_slots = num_slots;
+  const int rows[3] = {I, I, H}, Ks[3] = {H, H, I};
+  auto a256 = [](long long v) { return (v + 255) & ~255LL; };
+  long long off = 0;
+  for (int m = 0; m < 3; ++m) {
+    L.ld_scale[m] = (4 * fp8_blocks(Ks[m]) + 15) / 16 * 16;
+    L.codes_off[m] = off;
+    off = a256(off + (long long)rows[m] * Ks[m]);
+    L.scales_off[m] = off;
+    off = a256(off + (long long)fp8_blocks(rows[m]) * L.ld_scale[m]);
+  }
+  for (int m = 0; m < 3; ++m) L.global_off[m] = off + 4 * m;
+  L.slot_bytes = a256(off + 12);
+  L.scale_format = FT_SCALE_FP8;
+  *out = L;
+  return FT_OK;
+}
+
 extern "C" int ft_mxfp4_slot_layout_init(int H, int I, int num_slots, ft_nvfp4_slot_layout* out) {
   const int rc = ft_nvfp4_slot_layout_init(H, I, num_slots, out);
   if (rc == FT_OK) out->scale_format = FT_SCALE_MXFP4;
@@ -98,7 +122,8 @@ extern "C" int ft_tiled_slot_layout_init(int H, int I, int num_slots, int scale_
 static bool layout_ok(const ft_nvfp4_slot_layout* L) {
   return L && L->H > 0 && L->I > 0 && L->H % 64 == 0 && L->I % 64 == 0 && L->num_slots >= 1 &&
          L->slot_bytes % 256 == 0 && (L->tiled == 0 || L->tiled == 1) &&
-         (L->scale_format == FT_SCALE_NVFP4 || L->scale_format == FT_SCALE_MXFP4);
+         (L->scale_format == FT_SCALE_NVFP4 || L->scale_format == FT_SCALE_MXFP4 ||
+          (L->scale_format == FT_SCALE_FP8 && L->tiled == 0));
 }
 
 extern "C" int ft_moe_route(const float* logits, int T, int E, int k, int mode, int32_t* ids, float* w,
@@ -275,6 +300,12 @@ extern "C" int ft_pack_slot(const float* w, int mat, const ft_nvfp4_slot_layout*
     return fail(FT_ERR_INVALID_ARG, "ft_pack_slot: w must be 16-byte and the slot 256-byte aligned");
   const int N = mat == FT_DOWN ? L->H : L->I, K = mat == FT_DOWN ? L->I : L->H;
   uint8_t* base = static_cast<uint8_t*>(slot);
+  if (L->scale_format == FT_SCALE_FP8) {
+    const cudaError_t e = launch_fp8_pack(w, N, K, base + L->codes_off[mat], K,
+                                          reinterpret_cast<float*>(base + L->scales_off[mat]), L->ld_scale[mat] / 4,
+                                          S(stream));
+    return e == cudaSuccess ? FT_OK : cuda_fail(e, "ft_pack_slot");
+  }
   PackPlace pl;
   pl.codes = base + L->codes_off[mat];
   pl.scales = base + L->scales_off[mat];
@@ -300,6 +331,144 @@ extern "C" int ft_mxfp4_pack(const float* w, int N, int K, uint8_t* codes, uint8
   const cudaError_t e = launch_pack_mxfp4(w, N, K, row_major_place(codes, scales, K, ld_scale), ld_scale,
                                           global_scale, ws, S(stream));
   return e == cudaSuccess ? FT_OK : cuda_fail(e, "ft_mxfp4_pack");
+}
+
+static bool float_type_ok(int t) { return t == FT_F32 || t == FT_BF16 || t == FT_F16; }
+static bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+extern "C" int ft_fp8_quant_rows(const void* x, int x_type, int M, int K, int64_t ld_x, uint8_t* codes,
+                                 int64_t ld_codes, float* scales, int64_t ld_scales, ft_stream_t stream) {
+  if (M < 0 || K < 1 || !float_type_ok(x_type) || ld_x < K || ld_codes < K || ld_codes % 16 ||
+      ld_scales < fp8_blocks(K) || (long long)M * fp8_blocks(K) >= (1LL << 31))
+    return fail(FT_ERR_INVALID_ARG,
+                "ft_fp8_quant_rows: need M >= 0, K >= 1, a float type, pitches that hold a row, ld_codes % 16 == 0");
+  if (M == 0) return FT_OK;
+  if (!x || !codes || !scales) return fail(FT_ERR_INVALID_ARG, "ft_fp8_quant_rows: null pointer");
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(x, x_type == FT_F32 ? 4 : 2))
+    return fail(FT_ERR_INVALID_ARG, "ft_fp8_quant_rows: misaligned pointer (codes must be 16-byte aligned)");
+  const cudaError_t e = launch_fp8_quant(x, x_type, M, K, ld_x, codes, ld_codes, scales, ld_scales, S(stream));
+  return e == cudaSuccess ? FT_OK : cuda_fail(e, "ft_fp8_quant_rows");
+}
+
+extern "C" int ft_fp8_pack(const float* w, int N, int K, uint8_t* codes, int64_t ld_codes, float* scales,
+                           int ld_scales, ft_stream_t stream) {
+  if (N < 1 || K < 1 || ld_codes < K || ld_codes % 16 || ld_scales < fp8_blocks(K) || fp8_blocks(N) > 65535)
+    return fail(FT_ERR_INVALID_ARG,
+                "ft_fp8_pack: need N, K >= 1, ld_codes >= K and a multiple of 16, ld_scales >= ceil(K/128)");
+  if (!w || !codes || !scales) return fail(FT_ERR_INVALID_ARG, "ft_fp8_pack: null pointer");
+  if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(w, 4))
+    return fail(FT_ERR_INVALID_ARG, "ft_fp8_pack: misaligned pointer (codes must be 16-byte aligned)");
+  const cudaError_t e = launch_fp8_pack(w, N, K, codes, ld_codes, scales, ld_scales, S(stream));
+  return e == cudaSuccess ? FT_OK : cuda_fail(e, "ft_fp8_pack");
+}
+
+static bool fp8_gemm_shape_ok(int M, int N, int K) {
+  return M >= 0 && N >= 1 && K >= 1 && M <= (1 << 24) && N <= (1 << 24) && K < (1 << 24);
+}
+
+extern "C" size_t ft_fp8_gemm_workspace_size(int M, int N, int K) {
+  if (M <= 0 || !fp8_gemm_shape_ok(M, N, K)) return 0;
+  return fp8_gemm_ws_bytes(M, N, K);
+}
+
+extern "C" int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64_t ld_sa, const uint8_t* b,
+                           int64_t ldb, const float* sb, int64_t ld_sb, int M, int N, int K, void* out, int out_type,
+                           int64_t ldo, void* ws, size_t ws_bytes, ft_stream_t stream) {
+  if (!fp8_gemm_shape_ok(M, N, K) || lda < K || ldb < K || lda % 16 || ldb % 16 || ld_sa < fp8_blocks(K) ||
+      ld_sb < fp8_blocks(K) || ldo < N || (out_type != FT_F32 && out_type != FT_BF16))
+    return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: need N, K >= 1 (M, N, K up to 2^24), code pitches that hold a row and "
+                                    "are multiples of 16, scale and output pitches that hold a row, out_type f32 or bf16");
+  if (M == 0) return FT_OK;
+  if (!a || !sa || !b || !sb || !out) return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: null pointer");
+  if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4) ||
+      !aligned(out, out_type == FT_F32 ? 4 : 2) || !aligned(ws, 256))
+    return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: misaligned pointer (codes 16-byte, ws 256-byte)");
+  const size_t need = fp8_gemm_ws_bytes(M, N, K);
+  if (need > 0 && (!ws || ws_bytes < need)) return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: workspace too small");
+  const char* why = "ft_fp8_gemm";
+  const cudaError_t e = launch_fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo, ws,
+                                        S(stream), &why);
+  return e == cudaSuccess ? FT_OK : cuda_fail(e, why);
+}
+
+extern "C" size_t ft_moe_ffn_fp8_workspace_size(int T, int H, int I, int E, int k) {
+  if (T <= 0 || !ffn_shape_ok(H, I, E, k) || (long long)T * k > (1 << 24)) return 0;
+  return plan_fp8_ffn(T, H, I, E, k).total;
+}
+
+extern "C" int ft_moe_ffn_fp8(const void* x, int T, int H, int I, int E, int k, const int32_t* perm_src,
+                              const int32_t* expert_offsets, const int32_t* slot_table, const void* slot_pool,
+                              const ft_nvfp4_slot_layout* layout, void* out_perm, int out_type, void* ws,
+                              size_t ws_bytes, ft_stream_t stream) {
+  if (T < 0 || !ffn_shape_ok(H, I, E, k) || (long long)T * k > (1 << 24))
+    return fail(FT_ERR_UNSUPPORTED,
+                "ft_moe_ffn_fp8: need H, I >= 256 and multiples of 64, 1 <= k <= E <= 1024, T*k <= 2^24");
+  if (out_type != FT_F32 && out_type != FT_BF16)
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_ffn_fp8: out_type must be f32 or bf16");
+  if (T == 0) return FT_OK;
+  if (!x || !perm_src || !expert_offsets || !slot_table || !slot_pool || !layout || !out_perm || !ws)
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_ffn_fp8: null pointer");
+  if (!layout_ok(layout) || layout->scale_format != FT_SCALE_FP8 || layout->H != H || layout->I != I ||
+      layout->num_slots > (1 << 21))
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_ffn_fp8: the layout is not an FP8 layout of H, I (or has more than 2^21 slots)");
+  if (!aligned(slot_pool, 256) || !aligned(ws, 256) || !aligned(x, 16) || !aligned(out_perm, 16))
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_ffn_fp8: misaligned pointer");
+  if (ws_bytes < plan_fp8_ffn(T, H, I, E, k).total)
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_ffn_fp8: workspace too small");
+  const char* why = "ft_moe_ffn_fp8";
+  const cudaError_t e = launch_fp8_ffn(x, T, H, I, E, k, perm_src, expert_offsets, slot_table, slot_pool, *layout,
+                                       out_perm, out_type, ws, S(stream), &why);
+  return e == cudaSuccess ? FT_OK : cuda_fail(e, why);
+}
+
+extern "C" int ft_moe_combine_bf16(const void* out_perm, const int32_t* pair_to_row, const float* w, int T, int k,
+                                   int H, void* y, ft_stream_t stream) {
+  if (T < 0 || k < 1 || k > 1024 || H < 8 || H % 8)
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_combine_bf16: need k >= 1 and H a positive multiple of 8");
+  if (T == 0) return FT_OK;
+  if (!out_perm || !pair_to_row || !w || !y) return fail(FT_ERR_INVALID_ARG, "ft_moe_combine_bf16: null pointer");
+  if (!aligned(out_perm, 16) || !aligned(y, 16))
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_combine_bf16: out_perm and y must be 16-byte aligned");
+  const cudaError_t e = launch_combine_bf16(out_perm, pair_to_row, w, T, k, H, y, S(stream));
+  return e == cudaSuccess ? FT_OK : cuda_fail(e, "ft_moe_combine_bf16");
+}
+
+static bool balance_shape_ok(int T, int E, int k) {
+  return T >= 0 && E >= 1 && E <= 1024 && k >= 1 && k <= E && k <= 32 && (long long)T * k <= (1LL << 30);
+}
+
+extern "C" size_t ft_moe_balance_workspace_size(int T, int E) {
+  if (T <= 0 || E < 1 || E > 1024) return 0;
+  return balance_ws_bytes(T, E, device_sm_count());
+}
+
+extern "C" int ft_moe_balance(const float* logits, int64_t ld, const int32_t* ids, const uint8_t* valid, int T, int E,
+                              int k, float coef, int32_t* counts, int32_t* n_valid, float* loss, void* ws,
+                              size_t ws_bytes, ft_stream_t stream) {
+  if (!balance_shape_ok(T, E, k) || ld < E)
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_balance: need 1 <= k <= min(E, 32), E <= 1024, ld >= E");
+  if (!counts || !n_valid || !loss || (T > 0 && (!logits || !ids)))
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_balance: null pointer");
+  if (T > 0 && (!ws || ws_bytes < balance_ws_bytes(T, E, device_sm_count()) || !aligned(ws, 16)))
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_balance: workspace too small or misaligned");
+  const cudaError_t e = launch_balance(logits, ld, ids, valid, T, E, k, coef, counts, n_valid, loss, ws,
+                                       device_sm_count(), S(stream));
+  return e == cudaSuccess ? FT_OK : cuda_fail(e, "ft_moe_balance");
+}
+
+extern "C" int ft_moe_route_backward(const float* logits, int64_t ld, const int32_t* ids, const float* w,
+                                     const float* dw, const uint8_t* valid, int T, int E, int k, float coef,
+                                     const int32_t* counts, const int32_t* n_valid, const float* dloss, float* dlogits,
+                                     int64_t ldd, ft_stream_t stream) {
+  if (!balance_shape_ok(T, E, k) || (counts && ld < E) || ldd < E)
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_route_backward: need 1 <= k <= min(E, 32), E <= 1024, pitches >= E");
+  if (!counts && !dw) return fail(FT_ERR_INVALID_ARG, "ft_moe_route_backward: neither counts nor dw given");
+  if (T == 0) return FT_OK;
+  if (!dlogits || (counts && (!logits || !n_valid)) || (dw && (!w || !ids)))
+    return fail(FT_ERR_INVALID_ARG, "ft_moe_route_backward: null pointer");
+  const cudaError_t e = launch_route_backward(logits, ld, ids, w, dw, valid, T, E, k, coef, counts, n_valid, dloss,
+                                              dlogits, ldd, device_sm_count(), S(stream));
+  return e == cudaSuccess ? FT_OK : cuda_fail(e, "ft_moe_route_backward");
 }
 
 extern "C" int ft_device_status(int* status, int clear) {

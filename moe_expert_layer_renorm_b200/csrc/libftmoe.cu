@@ -17,6 +17,9 @@
 #include "selftest.cu"
 #include "ffn_host.cu"
 #include "layer.cu"
+#include "fp8_quant.cu"
+#include "fp8_gemm.cu"
+#include "balance.cu"
 #include "api.cu"
 #include "permute_noalloc.cu"
 #include "slots.cpp"

@@ -33,18 +33,23 @@ def untile(block: np.ndarray, N: int, width: int, row_bytes: int) -> np.ndarray:
 
 
 class ExpertPool:
-    """A device pool of expert slots (NVFP4, or MXFP4 with fmt=FT_SCALE_MXFP4),
-    row-major or stage-tiled (tiled=True; see ft_tiled_slot_layout_init)."""
+    """A device pool of expert slots (NVFP4, or MXFP4 with fmt=FT_SCALE_MXFP4,
+    FP8 with fmt=FT_SCALE_FP8), row-major or stage-tiled (tiled=True; see
+    ft_tiled_slot_layout_init; not for FP8).  ``buf``: the slots' bytes, for a
+    pool that is already filled."""
 
     def __init__(self, H: int, I: int, num_slots: int, device="cuda", fmt: int = _lib.FT_SCALE_NVFP4,
-                 tiled: bool = False):
+                 tiled: bool = False, buf: Optional[torch.Tensor] = None):
         self.H, self.I, self.num_slots, self.fmt, self.tiled = H, I, num_slots, fmt, tiled
         self.layout = _lib.slot_layout(H, I, num_slots, fmt, tiled)
         # the canonical row-major layout of the same format, for slots read back to the host
         self.rows_layout = _lib.slot_layout(H, I, num_slots, fmt)
         self.slot_bytes = int(self.layout.slot_bytes)
-        self.buf = torch.zeros(num_slots * self.slot_bytes, dtype=torch.uint8, device=device)
-        self._pack_ws = torch.zeros(256, dtype=torch.uint8, device=device)
+        if buf is None:
+            buf = torch.zeros(num_slots * self.slot_bytes, dtype=torch.uint8, device=device)
+        assert buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() == num_slots * self.slot_bytes
+        self.buf = buf
+        self._pack_ws = torch.zeros(256, dtype=torch.uint8, device=buf.device)
 
     @property
     def ptr(self) -> int:
@@ -58,7 +63,7 @@ class ExpertPool:
         N, K = self.shape(mat)
         assert w.shape == (N, K) and w.dtype == torch.float32 and w.is_cuda and w.is_contiguous()
         base = self.ptr + slot * self.slot_bytes
-        if self.tiled:
+        if self.tiled or self.fmt == _lib.FT_SCALE_FP8:
             _lib.pack_slot(w.data_ptr(), mat, self.layout, base, self._pack_ws.data_ptr(), _stream(stream))
             return
         L = self.layout
@@ -70,11 +75,17 @@ class ExpertPool:
         return self.buf[slot * self.slot_bytes:(slot + 1) * self.slot_bytes]
 
     def tensor_bytes(self, slot: int, mat: int):
-        """(codes uint8 [N, K/2], scales uint8 [N, ld], global fp32) of one tensor, on the host, row-major."""
+        """(codes uint8 [N, K/2], scales uint8 [N, ld], global fp32) of one tensor, on the host, row-major;
+        FP8: (codes uint8 [N, K], scales fp32 [ceil(N/128), ceil(K/128)], 1.0)."""
         N, K = self.shape(mat)
         L = self.layout
         ld = L.ld_scale[mat]
         s = self.slot_view(slot)
+        if self.fmt == _lib.FT_SCALE_FP8:
+            nb, kb = (N + 127) // 128, (K + 127) // 128
+            codes = s[L.codes_off[mat]:L.codes_off[mat] + N * K].view(N, K).cpu().numpy()
+            scales = s[L.scales_off[mat]:L.scales_off[mat] + nb * ld].cpu().numpy().view("float32").reshape(nb, ld // 4)
+            return codes, np.ascontiguousarray(scales[:, :kb]), 1.0
         if self.tiled:
             S = (K + 255) // 256
             codes = untile(s[L.codes_off[mat]:L.codes_off[mat] + S * N * 128].cpu().numpy(), N, 128, K // 2)
@@ -101,10 +112,15 @@ class ExpertPool:
 
 
 class MoELayer:
-    """Buffers and calls for one MoE FFN layer of fixed (T, E, k, H, I)."""
+    """Buffers and calls for one MoE FFN layer of fixed (T, E, k, H, I).
+
+    ffn() and forward() take NVFP4, MXFP4 and FP8 pools.  out_dtype is the type
+    of the expert outputs out_perm: torch.float32, or for FP8 pools also
+    torch.bfloat16."""
 
     def __init__(self, T: int, E: int, k: int, H: int, I: int, mode: int = _lib.FT_ROUTE_SOFTMAX_RENORM,
-                 device="cuda", fused_front: bool = False, whole: bool = False):
+                 device="cuda", fused_front: bool = False, whole: bool = False, out_dtype=torch.float32):
+        assert out_dtype in (torch.float32, torch.bfloat16)
         self.T, self.E, self.k, self.H, self.I, self.mode = T, E, k, H, I, mode
         self.fused_front = fused_front   # route + permute through ft_moe_route_permute (separate calls only)
         # forward() through ft_moe_layer_nvfp4 (one launch for decode-sized batches); False: the four calls
@@ -117,13 +133,14 @@ class MoELayer:
         self.offsets = torch.empty(E + 1, **i32)
         self.perm_src = torch.empty(P, **i32)
         self.pair_to_row = torch.empty(P, **i32)
-        self.out_perm = torch.empty((P, H), dtype=torch.float32, device=dev)
+        self.out_perm = torch.empty((P, H), dtype=out_dtype, device=dev)
         self.y = torch.empty((T, H), dtype=torch.float32, device=dev)
         self.dev = dev
         self.perm_ws_bytes = _lib.permute_workspace_size(T, k, E)
         self.ffn_ws_bytes = _lib.ffn_workspace_size(T, H, I, E, k)
         self.layer_ws_bytes = _lib.layer_workspace_size(T, H, I, E, k)
-        self._perm_ws = self._ffn_ws = self._layer_ws = None
+        self.fp8_ws_bytes = _lib.ffn_fp8_workspace_size(T, H, I, E, k)
+        self._perm_ws = self._ffn_ws = self._layer_ws = self._fp8_ws = None
 
     # workspaces, allocated on first use: the separate calls' (permute, ffn) and
     # the whole-layer call's, which is zero-filled once and left ready by every call
@@ -138,6 +155,12 @@ class MoELayer:
         if self._ffn_ws is None:
             self._ffn_ws = torch.empty(max(self.ffn_ws_bytes, 256), dtype=torch.uint8, device=self.dev)
         return self._ffn_ws
+
+    @property
+    def fp8_ws(self) -> torch.Tensor:
+        if self._fp8_ws is None:
+            self._fp8_ws = torch.empty(max(self.fp8_ws_bytes, 256), dtype=torch.uint8, device=self.dev)
+        return self._fp8_ws
 
     @property
     def layer_ws(self) -> torch.Tensor:
@@ -159,13 +182,22 @@ class MoELayer:
                            self.pair_to_row.data_ptr(), self.perm_ws.data_ptr(), self.perm_ws_bytes, _stream(stream))
 
     def ffn(self, x: torch.Tensor, slot_table: torch.Tensor, pool: ExpertPool, stream=None) -> None:
+        if pool.fmt == _lib.FT_SCALE_FP8:
+            _lib.ffn_fp8(x.data_ptr(), self.T, self.H, self.I, self.E, self.k, self.perm_src.data_ptr(),
+                         self.offsets.data_ptr(), slot_table.data_ptr(), pool.ptr, pool.layout,
+                         self.out_perm.data_ptr(),
+                         _lib.FT_F32 if self.out_perm.dtype == torch.float32 else _lib.FT_BF16,
+                         self.fp8_ws.data_ptr(), self.fp8_ws_bytes, _stream(stream))
+            return
+        assert self.out_perm.dtype == torch.float32, "bf16 expert outputs are for FP8 pools"
         _lib.ffn_nvfp4(x.data_ptr(), self.T, self.H, self.I, self.E, self.k, self.perm_src.data_ptr(),
                        self.offsets.data_ptr(), slot_table.data_ptr(), pool.ptr, pool.layout,
                        self.out_perm.data_ptr(), self.ffn_ws.data_ptr(), self.ffn_ws_bytes, _stream(stream))
 
     def combine(self, stream=None) -> None:
-        _lib.combine(self.out_perm.data_ptr(), self.pair_to_row.data_ptr(), self.w.data_ptr(), self.T, self.k,
-                     self.H, self.y.data_ptr(), _stream(stream))
+        combine = _lib.combine if self.out_perm.dtype == torch.float32 else _lib.combine_bf16
+        combine(self.out_perm.data_ptr(), self.pair_to_row.data_ptr(), self.w.data_ptr(), self.T, self.k, self.H,
+                self.y.data_ptr(), _stream(stream))
 
     def layer(self, x: torch.Tensor, logits: torch.Tensor, slot_table: torch.Tensor, pool: ExpertPool,
               stream=None) -> None:
@@ -178,11 +210,11 @@ class MoELayer:
     def forward(self, x: torch.Tensor, logits: torch.Tensor, slot_table: torch.Tensor, pool: ExpertPool,
                 stream=None) -> torch.Tensor:
         """route -> permute -> ffn -> combine, enqueued on one stream (one ft_moe_layer_nvfp4 call, or
-        the four calls when the layer was made with whole=False)."""
+        the four calls when the layer was made with whole=False or the pool holds FP8 experts)."""
         assert x.dtype == torch.bfloat16 and x.shape == (self.T, self.H) and x.is_contiguous()
         assert logits.dtype == torch.float32 and logits.shape == (self.T, self.E) and logits.is_contiguous()
         assert slot_table.dtype == torch.int32 and slot_table.numel() == self.E
-        if self.whole:
+        if self.whole and pool.fmt != _lib.FT_SCALE_FP8:
             self.layer(x, logits, slot_table, pool, stream)
             return self.y
         if self.fused_front:
