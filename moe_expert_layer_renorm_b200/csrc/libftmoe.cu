@@ -1,6 +1,7 @@
 // libftmoe.so is built as a single translation unit: the device status word
 // and the kernels share one module, and no relocatable device code is needed.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
