@@ -92,7 +92,12 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)
       : "r"(taddr) : "memory");
 }
 
-__device__ __forceinline__ float fp8_silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) u with the hardware exponential and a fast divide: a few fp32 steps
+// (as the exponential overflows the quotient goes to 0, its limit).  One h a
+// thread and column stands between a tile's last block and the next tile's
+// first: with expf and two IEEE divisions here the gate/up kernel of 4096
+// skewed tokens took 259 us instead of 176.
+__device__ __forceinline__ float fp8_silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 __device__ __forceinline__ void store_as(void* out, int type, size_t i, float v) {
   if (type == FT_F32) static_cast<float*>(out)[i] = v;
@@ -120,6 +125,26 @@ struct Fp8StreamCfg {
 };
 
 constexpr int kFp8StreamThreads = 192;   // TMA warp, MMA warp, four epilogue warps
+// One lane of a converged warp.  The MMA warps run their loops as a whole warp
+// with warp-uniform values and issue inside this branch: descriptors and
+// addresses then stay in uniform registers.  (Four MMAs of N = 32, their two
+// commits and two passed waits take 333 cycles to issue this way, 528 from a
+// loop of lane 0 alone -- more than the 512 the four MMAs of N = 256 run.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred q;\n elect.sync _|q, 0xFFFFFFFF;\n selp.b32 %0, 1, 0, q;\n}" : "=r"(p));
+  return p != 0;
+}
+
+// Whether the phase is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+               " selp.b32 %0, 1, 0, p;\n}"
+               : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+
 constexpr int kTagEpi = 9;               // barrier kind of a wait timeout: the epilogue warps' own barrier
 
 // A barrier of the epilogue warps: an mbarrier, so that a warp that has given
@@ -156,7 +181,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   int* last_flag = abort_flag + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp-uniform
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 4); }
@@ -173,7 +198,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   __syncthreads();
   tc_fence_after();
   pdl_wait();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const Abort ab{abort_flag};
 
   // this CTA's range of K blocks, all tiles' blocks in one line
@@ -207,19 +232,19 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
     }
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issuer ---
-    if (lane == 0) {
-      uint32_t i = 0;
-      bool ok = true;
-      int u = int(g0 / nk), kb = int(g0 - (long long)u * nk);
-      for (long long g = g0; g < g1 && ok; ++u, kb = 0) {
-        const int n_eff = (fp8_unit(p, u, BN).nr + 15) & ~15;
-        const uint32_t idesc = make_idesc_e4m3(128, n_eff);
-        for (; kb < nk && g < g1; ++kb, ++g, ++i) {
-          const int s = i % NST, b = i % DB;
-          ok = ab.wait(&d_empty[b], ((i / DB) & 1) ^ 1, kTagDEmpty, i, u) &&
-               ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, u);
-          if (!ok) break;
-          tc_fence_after();
+    uint32_t i = 0;
+    int s = 0, b = 0;
+    bool ok = true;
+    int u = int(g0 / nk), kb = int(g0 - (long long)u * nk);
+    for (long long g = g0; g < g1 && ok; ++u, kb = 0) {
+      const int n_eff = (fp8_unit(p, u, BN).nr + 15) & ~15;
+      const uint32_t idesc = make_idesc_e4m3(128, n_eff);
+      for (; kb < nk && g < g1; ++kb, ++g, ++i) {
+        ok = ab.wait(&d_empty[b], ((i / DB) & 1) ^ 1, kTagDEmpty, i, u) &&
+             ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, u);
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+        tc_fence_after();
+        if (elect_one()) {
           uint8_t* src = smem + s * Cfg::kStageBytes;
           const uint64_t rd = make_sdesc_sw128(smem_u32(src + NMAT * kFp8WBytes));
 #pragma unroll
@@ -232,12 +257,16 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
           mma_commit(&empty[s]);
           mma_commit(&d_full[b]);
         }
+        __syncwarp();
+        if (++s == NST) s = 0;
+        if (++b == DB) b = 0;
       }
-      if (i > 0) {   // drain: every MMA this thread issued has completed
-        mma_commit(drain_bar);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < 1000000000ull) {}
-      }
+    }
+    if (i > 0) {   // drain: every MMA this warp issued has completed
+      if (elect_one()) mma_commit(drain_bar);
+      __syncwarp();
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < 1000000000ull) {}
     }
   } else {
     // ---------------------------------------------------- epilogue ---
@@ -348,7 +377,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
           if (n >= d.nr) break;
           const uint32_t m = max(max(tmax[n], tmax[BN + n]), max(tmax[2 * BN + n], tmax[3 * BN + n]));
           const Fp8Scale f = fp8_scale_of(__uint_as_float(m));
-          if (feat < p.N) h[(d.rb + n) * p.ldo + feat] = uint8_t(cvt_e4m3x2(fp8_quotient(acc[0][n], f), 0.0f));
+          if (feat < p.N) h[(d.rb + n) * p.ldo + feat] = uint8_t(cvt_e4m3x2(acc[0][n] * fp8_factor_of(f), 0.0f));
           if (row == 0) p.hs[(long long)(d.rb + n) * hb + d.ft] = f.scale;
         }
         if (!(ok = epi.sync(lane))) break;   // the maxima are read before the next tile's are written
@@ -369,7 +398,9 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
 constexpr int kFp8TileThreads = 384;   // TMA warp, MMA warp, two idle; two epilogue warpgroups
 constexpr int kFp8TileStages = 4;
 constexpr int kFp8TileStageBytes = 3 * 128 * 128;
-constexpr int kFp8TileSmemBytes = 1024 + kFp8TileStages * kFp8TileStageBytes + (2 * kFp8TileStages + 6) * 8 + 2 * 256 * 4 + 32;
+constexpr int kFp8TileOutBytes = 8 * 4096;   // output staging of the eight epilogue warps; for gate/up the row maxima
+constexpr int kFp8TileSmemBytes =
+    1024 + kFp8TileStages * kFp8TileStageBytes + kFp8TileOutBytes + (2 * kFp8TileStages + 6) * 8 + 32;
 
 __device__ __forceinline__ unsigned long long pack2(uint32_t lo, uint32_t hi) {
   unsigned long long r;
@@ -389,20 +420,21 @@ template <int NMAT>
 __global__ void __launch_bounds__(kFp8TileThreads, 1)
 fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
                 const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_rows) {
-  constexpr int NST = kFp8TileStages, DB = 2;
+  constexpr int NST = kFp8TileStages, DB = 2;   // DB: accumulator buffers
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NST * kFp8TileStageBytes);
+  uint8_t* out_stage = smem + NST * kFp8TileStageBytes;
+  uint32_t* tmax = reinterpret_cast<uint32_t*>(out_stage);   // [unit parity][half][128]
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + kFp8TileOutBytes);
   uint64_t* empty = full + NST;
   uint64_t* d_full = empty + NST;
   uint64_t* d_empty = d_full + DB;
   uint64_t* drain_bar = d_empty + DB;
   uint64_t* epi_bar = drain_bar + 1;
-  uint32_t* tmax = reinterpret_cast<uint32_t*>(epi_bar + 1);   // [unit parity][half][128]
-  uint32_t* tmem_slot = tmax + 512;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp-uniform
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 8); }
@@ -419,14 +451,14 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   __syncthreads();
   tc_fence_after();
   pdl_wait();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const Abort ab{abort_flag};
   const int nk = p.nk;
   const int n_units = p.units ? *p.num_units : p.row_tiles * p.feat_tiles;
 
-  // registers: 384 threads x 168 at launch = 128 x 72 + 256 x 216
+  // registers: 384 threads x 168 at launch = 128 x 56 + 256 x 224
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       // ---------------------------------------------- TMA producer ---
       if (lane == 0) {
@@ -440,11 +472,15 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
             uint8_t* dst = smem + s * kFp8TileStageBytes;
             mbar_arrive_expect_tx(&full[s], kFp8TileStageBytes);
             tma_load_2d(dst, &tm_rows, &full[s], kb * 128, d.rb);
-            if (NMAT == 2) {   // 128 gate rows, then the 128 up rows of the same features
-              tma_load_3d(dst + kFp8WBytes, &tm_w0, &full[s], kb * 128, d.ft * 128, d.slot);
-              tma_load_3d(dst + 2 * kFp8WBytes, &tm_w1, &full[s], kb * 128, d.ft * 128, d.slot);
+            uint8_t* wdst = dst + kFp8WBytes;
+            if (NMAT == 2) {   // each half: 64 gate rows, then the up rows of the same 64 features
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                tma_load_3d(wdst + h * kFp8WBytes, &tm_w0, &full[s], kb * 128, d.ft * 128 + h * 64, d.slot);
+                tma_load_3d(wdst + h * kFp8WBytes + kFp8WBytes / 2, &tm_w1, &full[s], kb * 128, d.ft * 128 + h * 64, d.slot);
+              }
             } else {           // one box of 256 rows
-              tma_load_3d(dst + kFp8WBytes, &tm_w0, &full[s], kb * 128, d.ft * 256, d.slot);
+              tma_load_3d(wdst, &tm_w0, &full[s], kb * 128, d.ft * 256, d.slot);
             }
           }
         }
@@ -455,40 +491,48 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
       }
     } else if (warp == 1) {
       // ----------------------------------------------- MMA issuer ---
-      if (lane == 0) {
-        constexpr uint32_t idesc = make_idesc_e4m3(128, 256);
-        uint32_t i = 0;
-        bool ok = true;
-        for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-          for (int kb = 0; kb < nk; ++kb, ++i) {
-            const int s = i % NST, b = i % DB;
-            ok = ab.wait(&d_empty[b], ((i / DB) & 1) ^ 1, kTagDEmpty, i, u) &&
-                 ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, u);
-            if (!ok) break;
-            tc_fence_after();
+      // The barriers of the next block are tried right after this block's MMAs
+      // are issued, both at once: a try_wait takes some 85 cycles to answer
+      // even when its phase is complete.
+      constexpr uint32_t idesc = make_idesc_e4m3(128, 256);
+      uint32_t i = 0;
+      int s = 0, b = 0;
+      bool ok = true, tried = false, have_rows = false, have_d = false;
+      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
+        for (int kb = 0; kb < nk; ++kb, ++i) {
+          if (!tried || !have_rows) ok = ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, u);
+          if (!tried || !have_d) ok = ok && ab.wait(&d_empty[b], ((i / DB) & 1) ^ 1, kTagDEmpty, i, u);
+          if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+          tc_fence_after();
+          if (elect_one()) {
             const uint64_t rd = make_sdesc_sw128(smem_u32(smem + s * kFp8TileStageBytes));
             const uint64_t wd = make_sdesc_sw128(smem_u32(smem + s * kFp8TileStageBytes + kFp8WBytes));
 #pragma unroll
             for (int j = 0; j < 4; ++j) mma_ss_f8(tmem + b * 256, rd + 2 * j, wd + 2 * j, idesc, j > 0);
-            mma_commit(&empty[s]);
             mma_commit(&d_full[b]);
+            mma_commit(&empty[s]);
           }
+          __syncwarp();
+          if (++s == NST) s = 0;
+          b ^= 1;
+          have_rows = mbar_test_wait(&full[s], ((i + 1) / NST) & 1);
+          have_d = mbar_test_wait(&d_empty[b], (((i + 1) / DB) & 1) ^ 1);
+          tried = true;
         }
-        if (i > 0) {
-          mma_commit(drain_bar);
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < 1000000000ull) {}
-        }
+      }
+      if (i > 0) {   // drain
+        if (elect_one()) mma_commit(drain_bar);
+        __syncwarp();
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < 1000000000ull) {}
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // -------------------------------------------------- epilogue ---
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;                 // token row within the tile = tensor-memory lane
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
-    // columns: NMAT 1: half * 128 .. + 127; NMAT 2: 64 gate columns at half * 64 and 64 up columns at 128 + half * 64
-    const uint32_t col0 = NMAT == 2 ? half * 64 : half * 128, col1 = NMAT == 2 ? 128 + half * 64 : half * 128 + 64;
     EpiSync epi{epi_bar, ab, 0};
     uint32_t i = 0;
     bool ok = true;
@@ -502,68 +546,111 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
       const bool has = block * kFp8Block < p.N;
       const float* sw0 = fp8_weight_scales(p, 0, d.slot, has ? block : 0);
       const float* sw1 = NMAT == 2 ? fp8_weight_scales(p, 1, d.slot, block) : sw0;
-      unsigned long long acc[64];
+      unsigned long long acc[64];   // NMAT 1: 128 columns; NMAT 2: gate of 64 features, then up
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = 0ull;
-      float a = __ldg(sr), w0 = __ldg(sw0), w1 = __ldg(sw1);
+      float a = __ldg(sr), w0 = __ldg(sw0), w1 = NMAT == 2 ? __ldg(sw1) : 0.0f;
+      // Chunks of 32 columns in two register buffers, the next chunk's load in
+      // flight behind one chunk's sums -- also across blocks: the last chunk's
+      // sums stand behind the next block's first load.
+      uint32_t v[2][32];
+      if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[i & 1], (i >> 1) & 1, kTagDFull, i, u)))) break;
+      tc_fence_after();
+      const uint32_t dcol = tmem + lane_base + half * 128;
+      tmem_ld_32x32b_x32(dcol + (i & 1) * 256, v[0]);
       for (int kb = 0; kb < nk; ++kb, ++i) {
-        const int b = i % DB;
+        const uint32_t b = i & 1;
         const float s0 = a * w0, s1 = a * w1;
         const unsigned long long p0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
         const unsigned long long p1 = NMAT == 2 ? pack2(__float_as_uint(s1), __float_as_uint(s1)) : p0;
-        if (kb + 1 < nk) { a = __ldg(sr + kb + 1); w0 = __ldg(sw0 + kb + 1); w1 = __ldg(sw1 + kb + 1); }
-        if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[b], (i / DB) & 1, kTagDFull, i, u)))) break;
-        tc_fence_after();
-        const uint32_t dcol = tmem + lane_base + b * 256;
-        uint32_t v[2][32];
-        tmem_ld_32x32b_x32(dcol + col0, v[0]);
+        const bool more = kb + 1 < nk;
+        if (more) {
+          a = __ldg(++sr);
+          w0 = __ldg(++sw0);
+          if (NMAT == 2) w1 = __ldg(++sw1);
+        }
+        bool ready = false;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           tmem_wait_ld();
           if (c < 3) {
-            tmem_ld_32x32b_x32(dcol + (c < 1 ? col0 + 32 : col1 + (c - 1) * 32), v[(c + 1) & 1]);
+            tmem_ld_32x32b_x32(dcol + b * 256 + (c + 1) * 32, v[(c + 1) & 1]);
+            if (c == 1) ready = mbar_test_wait(&d_full[b ^ 1], ((i + 1) >> 1) & 1);
           } else {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[b]);
+            if (more) {
+              if (!ready) ok = ab.wait(&d_full[b ^ 1], ((i + 1) >> 1) & 1, kTagDFull, i + 1, u);
+              if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+              tc_fence_after();
+              tmem_ld_32x32b_x32(dcol + (b ^ 1) * 256, v[0]);
+            }
           }
 #pragma unroll
           for (int n = 0; n < 16; ++n) fma2(acc[c * 16 + n], pack2(v[c & 1][2 * n], v[c & 1][2 * n + 1]), c < 2 ? p0 : p1);
         }
+        if (!ok) break;
       }
       if (!ok) break;
       if constexpr (NMAT == 1) {
-        if (live) {
-          const int f0 = d.ft * 256 + half * 128;
-          const size_t at = (d.rb + row) * p.ldo + f0;
-          if (p.out_type == FT_BF16 && f0 + 128 <= p.N && p.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at);
+        // Through 4 KB of shared memory a warp, 64 bf16 or 32 fp32 columns of its
+        // 32 rows at a time: a thread has a row's columns, but stores of whole
+        // 128-byte rows, four rows an instruction, are what the memory takes
+        // well (16-byte stores to 32 rows took half of the unit's time).
+        uint8_t* stage = out_stage + (warp - 4) * 4096;
+        const int f0 = d.ft * 256 + half * 128;
+        const int esize = p.out_type == FT_F32 ? 4 : 2;
+        const bool vec = (p.ldo * esize) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              uint32_t o[4];
+        for (int c0 = 0; c0 < 128; c0 += 32) {
+          // 16-byte piece q of the thread's row at q ^ (row % 8)
+          const bool f32 = p.out_type == FT_F32;
+          if (f32) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float2 f = unpack2(acc[4 * c + q]);
-                const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
-                o[q] = *reinterpret_cast<const uint32_t*>(&t);
-              }
-              dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
-            }
-          } else if (p.out_type == FT_F32 && f0 + 128 <= p.N && p.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float2 x = unpack2(acc[2 * c]), y = unpack2(acc[2 * c + 1]);
-              dst[c] = make_float4(x.x, x.y, y.x, y.y);
+            for (int q = 0; q < 8; ++q) {
+              const float2 x = unpack2(acc[c0 / 2 + 2 * q]), y = unpack2(acc[c0 / 2 + 2 * q + 1]);
+              *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_float4(x.x, x.y, y.x, y.y);
             }
           } else {
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-              const float2 f = unpack2(acc[c]);
-              if (f0 + 2 * c < p.N) store_as(p.out, p.out_type, at + 2 * c, f.x);
-              if (f0 + 2 * c + 1 < p.N) store_as(p.out, p.out_type, at + 2 * c + 1, f.y);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 x = unpack2(acc[c0 / 2 + 4 * q + e]);
+                const __nv_bfloat162 t = __floats2bfloat162_rn(x.x, x.y);
+                o[e] = *reinterpret_cast<const uint32_t*>(&t);
+              }
+              const int piece = (c0 & 32) / 8 + q;
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            if (!(c0 & 32)) continue;
+          }
+          __syncwarp();
+          const int fc = f0 + (f32 ? c0 : c0 - 32);   // the chunk's first feature
+#pragma unroll
+          for (int r = 0; r < 32; r += 4) {
+            const int rr = r + (lane >> 3), piece = lane & 7;
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
+            const int tile_row = quarter * 32 + rr, f = fc + piece * (16 / esize);
+            if (tile_row >= d.nr || f >= p.N) continue;
+            uint8_t* dst = static_cast<uint8_t*>(p.out) + ((d.rb + tile_row) * p.ldo + f) * esize;
+            if (vec && f + 16 / esize <= p.N) {
+              *reinterpret_cast<uint4*>(dst) = x;
+            } else {
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                if (f32) {
+                  if (e < 4 && f + e < p.N) reinterpret_cast<uint32_t*>(dst)[e] = w[e & 3];
+                } else if (f + e < p.N) {
+                  reinterpret_cast<uint16_t*>(dst)[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
+                }
+              }
             }
           }
+          __syncwarp();
         }
       } else {
         // h of this thread's 64 features; its scale is the maximum over the row's 128 (those past N are zeros)
@@ -580,6 +667,7 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
         if (!(ok = epi.sync(lane))) break;
         m = max(m, tmax[parity * 256 + (half ^ 1) * 128 + row]);
         const Fp8Scale f = fp8_scale_of(__uint_as_float(m));
+        const float inv = fp8_factor_of(f);
         const int f0 = d.ft * 128 + half * 64;
         if (live) {
           if (half == 0) p.hs[(long long)(d.rb + row) * ((p.N + kFp8Block - 1) / kFp8Block) + d.ft] = f.scale;
@@ -590,7 +678,8 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
               uint32_t o[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                o[q] = fp8_codes4(h[16 * c + 4 * q], h[16 * c + 4 * q + 1], h[16 * c + 4 * q + 2], h[16 * c + 4 * q + 3], f);
+                o[q] = cvt_e4m3x2(h[16 * c + 4 * q] * inv, h[16 * c + 4 * q + 1] * inv) |
+                       (cvt_e4m3x2(h[16 * c + 4 * q + 2] * inv, h[16 * c + 4 * q + 3] * inv) << 16);
               dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }
@@ -827,7 +916,7 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
             make_fp8_map(w + pl.off_h, P, I, I, 1, 16, pl.bn, false, &tm_h);
   for (int m = 0; m < 3; ++m)
     ok = ok && make_fp8_map(pool + L.codes_off[m], rows[m], Ks[m], Ks[m], L.num_slots, L.slot_bytes,
-                            m == FT_DOWN && !stream ? 256 : 128, true, &tm[m]);
+                            stream ? 128 : m == FT_DOWN ? 256 : 64, true, &tm[m]);
   if (!ok) {
     *why = "ft_moe_ffn_fp8: cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;

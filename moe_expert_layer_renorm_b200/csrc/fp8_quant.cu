@@ -37,6 +37,10 @@ __device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
 __device__ __forceinline__ float fp8_quotient(float x, const Fp8Scale& f) {
   return __fdiv_rn(__fmul_rn(x * f.pre, kFp8Max), f.div);
 }
+// The same for values that fp32 arithmetic has just computed (h), by one
+// product with 448 / m: no tie of theirs is meant, and a quotient within
+// 2^-23 of one may go either way.
+__device__ __forceinline__ float fp8_factor_of(const Fp8Scale& f) { return __fdiv_rn(kFp8Max, f.div) * f.pre; }
 // Two values -> two E4M3 codes, the first in the low byte (nearest even,
 // saturating at 448; NaN -> 0x7F).
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
