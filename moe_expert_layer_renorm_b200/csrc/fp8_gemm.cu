@@ -44,6 +44,7 @@ struct Fp8Params {
   void* out;                  // [rows, N], pitch ldo; for gate/up the codes of h
   int out_type;
   long long ldo;
+  int out_tma;                // tile kernel: `out` has a tensor map
   float* hs;                  // gate/up: scales of h [rows, ceil(N/128)]
   float* partials;            // stream kernel: two tiles for each CTA
   int* counters;              // stream kernel: arrivals at each cut tile, zero between launches
@@ -145,7 +146,7 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-constexpr int kTagEpi = 9;               // barrier kind of a wait timeout: the epilogue warps' own barrier
+constexpr int kTagEpi = 9, kTagOut = 10;  // barrier kinds of a wait timeout: the epilogue warps' own, the output staging's
 
 // A barrier of the epilogue warps: an mbarrier, so that a warp that has given
 // up leaves no other waiting without a limit.
@@ -395,66 +396,156 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
 
 // --------------------------------------------------------- many rows ---
 
-constexpr int kFp8TileThreads = 384;   // TMA warp, MMA warp, two idle; two epilogue warpgroups
-constexpr int kFp8TileStages = 4;
-constexpr int kFp8TileStageBytes = 3 * 128 * 128;
-constexpr int kFp8TileOutBytes = 8 * 4096;   // output staging of the eight epilogue warps; for gate/up the row maxima
-constexpr int kFp8TileSmemBytes =
-    1024 + kFp8TileStages * kFp8TileStageBytes + kFp8TileOutBytes + (2 * kFp8TileStages + 6) * 8 + 32;
+// PAIR: two CTAs of a cluster take one tile of 256 token rows (cta_group::2):
+// each loads its own 128 rows and half of the 256 weight rows, so that a block
+// costs 32 KB of shared-memory writes and reads a CTA where one CTA alone
+// needs 48 KB of each for the same MMAs.
+constexpr int kFp8OutChunk = 128 * 128;   // staged output: 128 rows of 128 bytes (64 bf16 or 32 fp32 features)
 
-__device__ __forceinline__ unsigned long long pack2(uint32_t lo, uint32_t hi) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+template <int NMAT, bool PAIR>
+struct Fp8TileCfg {
+  static constexpr int kRows = PAIR ? 256 : 128;                // token rows a tile
+  static constexpr int kWRows = PAIR ? 128 : 256;               // weight rows this CTA loads
+  static constexpr int kStages = PAIR || NMAT == 2 ? 4 : 3;
+  static constexpr int kStageBytes = kFp8WBytes + kWRows * 128;
+  static constexpr int kOutBytes = NMAT == 2 ? 2048 : 4 * kFp8OutChunk;   // gate/up: row maxima; else two chunks a half
+  static constexpr int kBars = 2 * kStages + 2 * 4 + 2 + 4;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kOutBytes + kBars * 8 + 32;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+constexpr int kFp8TileThreads = 384;   // warps for TMA, MMA, output stores and waiting; two epilogue warpgroups
+
+__device__ __forceinline__ void fma2_to(unsigned long long& acc, uint32_t lo, uint32_t hi, unsigned long long s) {
+  acc = fma2(pack2(__uint_as_float(lo), __uint_as_float(hi)), s, acc);
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ float2 unpack2(unsigned long long v) {
-  uint32_t lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(v));
-  return make_float2(__uint_as_float(lo), __uint_as_float(hi));
+// The cluster address of `p`'s place in the shared memory of CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
 }
-__device__ __forceinline__ void fma2(unsigned long long& acc, unsigned long long a, unsigned long long b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+// An arrive on a barrier of the pair.  It says only that this warp's tensor
+// memory loads are done (they are waited for); a release at cluster scope
+// would hold the warp until all its memory traffic is visible to the peer,
+// some thousand cycles a block.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
-template <int NMAT>
+// The tensor-memory, TMA and MMA forms of one CTA or of a pair.  A pair's TMA
+// loads (each CTA into its own shared memory, no multicast) complete on the
+// leader's barrier; its commits arrive on both CTAs' barriers.
+template <bool PAIR>
+struct Fp8Pair {
+  static __device__ __forceinline__ void alloc(uint32_t* dst) {
+    if (PAIR) asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n"
+                           " tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(smem_u32(dst)) : "memory");
+    else { tmem_alloc(dst, 512); tmem_relinquish(); }
+  }
+  static __device__ __forceinline__ void dealloc(uint32_t tmem) {
+    if (PAIR) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    else tmem_dealloc(tmem, 512);
+  }
+  static __device__ __forceinline__ void load_2d(void* dst, const void* map, uint32_t bar, int x, int y) {
+    if (PAIR)
+      asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+                   " [%0], [%1, {%3, %4}], [%2];"
+                   ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+    else
+      asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                   " [%0], [%1, {%3, %4}], [%2];"
+                   ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y) : "memory");
+  }
+  static __device__ __forceinline__ void load_3d(void* dst, const void* map, uint32_t bar, int x, int y, int z) {
+    if (PAIR)
+      asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+                   " [%0], [%1, {%3, %4, %5}], [%2];"
+                   ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+    else
+      asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                   " [%0], [%1, {%3, %4, %5}], [%2];"
+                   ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+  }
+  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t accumulate) {
+    if (PAIR)
+      asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                   " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+                   ::"r"(d), "l"(a), "l"(b), "r"(make_idesc_e4m3(256, 128)), "r"(accumulate) : "memory");
+    else
+      mma_ss_f8(d, a, b, make_idesc_e4m3(128, 128), accumulate);
+  }
+  static __device__ __forceinline__ void commit(uint32_t bar) {
+    if (PAIR)
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                   ::"r"(bar), "h"(uint16_t(3)) : "memory");
+    else
+      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  }
+};
+
+// A box of shared memory (128-byte swizzled) to a 2-D tensor; one of the thread's bulk group.
+__device__ __forceinline__ void tma_store_2d(const void* map, const void* src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+               ::"l"(map), "r"(smem_u32(src)), "r"(x), "r"(y) : "memory");
+}
+
+template <int NMAT, bool PAIR>
 __global__ void __launch_bounds__(kFp8TileThreads, 1)
 fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
-                const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_rows) {
-  constexpr int NST = kFp8TileStages, DB = 2;   // DB: accumulator buffers
+                const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_rows,
+                const __grid_constant__ CUtensorMap tm_out) {
+  using Cfg = Fp8TileCfg<NMAT, PAIR>;
+  using Pair = Fp8Pair<PAIR>;
+  constexpr int NST = Cfg::kStages, DB = 2;   // DB: accumulator buffers
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* out_stage = smem + NST * kFp8TileStageBytes;
-  uint32_t* tmax = reinterpret_cast<uint32_t*>(out_stage);   // [unit parity][half][128]
-  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + kFp8TileOutBytes);
+  uint8_t* out_stage = smem + NST * Cfg::kStageBytes;
+  uint32_t* tmax = reinterpret_cast<uint32_t*>(out_stage);   // gate/up: [unit parity][half][128] row maxima
+  uint64_t* full = reinterpret_cast<uint64_t*>(out_stage + Cfg::kOutBytes);
   uint64_t* empty = full + NST;
-  uint64_t* d_full = empty + NST;
-  uint64_t* d_empty = d_full + DB;
-  uint64_t* drain_bar = d_empty + DB;
+  uint64_t* d_full = empty + NST;         // [buffer][half]
+  uint64_t* d_empty = d_full + 2 * DB;
+  uint64_t* drain_bar = d_empty + 2 * DB;
   uint64_t* epi_bar = drain_bar + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(epi_bar + 1);
+  uint64_t* out_full = epi_bar + 1;      // [half]
+  uint64_t* out_empty = out_full + 2;    // [half]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(out_empty + 2);
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp-uniform
+  const uint32_t rank = PAIR ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-    for (int i = 0; i < DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 8); }
+    for (int i = 0; i < 2 * DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], PAIR ? 8 : 4); }
     mbar_init(drain_bar, 1);
     mbar_init(epi_bar, 8);
+    for (int i = 0; i < 2; ++i) { mbar_init(&out_full[i], 4); mbar_init(&out_empty[i], 1); }
     *abort_flag = 0;
     fence_mbarrier_init();
     prefetch_tmap(&tm_w0);
     if (NMAT > 1) prefetch_tmap(&tm_w1);
     prefetch_tmap(&tm_rows);
   }
-  if (warp == 1) { tmem_alloc(tmem_slot, 512); tmem_relinquish(); }
+  if (warp == 1) Pair::alloc(tmem_slot);
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();   // the peer's barriers are in place
   tc_fence_after();
   pdl_wait();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const Abort ab{abort_flag};
   const int nk = p.nk;
   const int n_units = p.units ? *p.num_units : p.row_tiles * p.feat_tiles;
+  const int u0 = PAIR ? blockIdx.x / 2 : blockIdx.x, du = PAIR ? gridDim.x / 2 : gridDim.x;
 
   // registers: 384 threads x 168 at launch = 128 x 56 + 256 x 224
   if (warp < 4) {
@@ -464,215 +555,302 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
       if (lane == 0) {
         uint32_t i = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-          const Fp8Unit d = fp8_unit(p, u, 128);
+        for (int u = u0; u < n_units && ok; u += du) {
+          const Fp8Unit d = fp8_unit(p, u, Cfg::kRows);
           for (int kb = 0; kb < nk; ++kb, ++i) {
             const int s = i % NST;
             if (!(ok = ab.wait(&empty[s], ((i / NST) & 1) ^ 1, kTagWEmpty, i, u))) break;
-            uint8_t* dst = smem + s * kFp8TileStageBytes;
-            mbar_arrive_expect_tx(&full[s], kFp8TileStageBytes);
-            tma_load_2d(dst, &tm_rows, &full[s], kb * 128, d.rb);
+            uint8_t* dst = smem + s * Cfg::kStageBytes;
+            const uint32_t bar = PAIR ? cluster_addr(&full[s], 0) : smem_u32(&full[s]);
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], (PAIR ? 2 : 1) * Cfg::kStageBytes);
+            Pair::load_2d(dst, &tm_rows, bar, kb * 128, d.rb + rank * 128);
             uint8_t* wdst = dst + kFp8WBytes;
-            if (NMAT == 2) {   // each half: 64 gate rows, then the up rows of the same 64 features
+            // Half h's 128 columns: NMAT 1 features 128 h .. of the tile's 256, NMAT 2 gate, then up of features
+            // 64 h .. of its 128; of a pair's half, CTA 0 holds the first 64 columns' rows and CTA 1 the others'.
+            if (NMAT == 2 && PAIR) {
+              Pair::load_3d(wdst, rank ? &tm_w1 : &tm_w0, bar, kb * 128, d.ft * 128, d.slot);
+            } else if (NMAT == 2) {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                tma_load_3d(wdst + h * kFp8WBytes, &tm_w0, &full[s], kb * 128, d.ft * 128 + h * 64, d.slot);
-                tma_load_3d(wdst + h * kFp8WBytes + kFp8WBytes / 2, &tm_w1, &full[s], kb * 128, d.ft * 128 + h * 64, d.slot);
+                Pair::load_3d(wdst + h * kFp8WBytes, &tm_w0, bar, kb * 128, d.ft * 128 + h * 64, d.slot);
+                Pair::load_3d(wdst + h * kFp8WBytes + kFp8WBytes / 2, &tm_w1, bar, kb * 128, d.ft * 128 + h * 64, d.slot);
               }
-            } else {           // one box of 256 rows
-              tma_load_3d(wdst, &tm_w0, &full[s], kb * 128, d.ft * 256, d.slot);
+            } else if (PAIR) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+                Pair::load_3d(wdst + h * kFp8WBytes / 2, &tm_w0, bar, kb * 128, d.ft * 256 + h * 128 + rank * 64, d.slot);
+            } else {
+              Pair::load_3d(wdst, &tm_w0, bar, kb * 128, d.ft * 256, d.slot);
             }
           }
         }
-        for (uint32_t j = (i > NST ? i - NST : 0); j < i; ++j) {   // drain
+        // drain: the last copies have landed, as the MMAs that read them are done
+        for (uint32_t j = (i > NST ? i - NST : 0); j < i; ++j) {
           const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(&full[j % NST], (j / NST) & 1) && globaltimer_ns() - t0 < 1000000000ull) {}
+          while (!mbar_try_wait(&empty[j % NST], (j / NST) & 1) && globaltimer_ns() - t0 < 1000000000ull) {}
         }
       }
-    } else if (warp == 1) {
+    } else if (warp == 1 && rank == 0) {
       // ----------------------------------------------- MMA issuer ---
-      // The barriers of the next block are tried right after this block's MMAs
-      // are issued, both at once: a try_wait takes some 85 cycles to answer
-      // even when its phase is complete.
-      constexpr uint32_t idesc = make_idesc_e4m3(128, 256);
-      uint32_t i = 0;
+      // Each K block as two 128-column halves with accumulators of their own, so
+      // that half 0 is read back while half 1 is multiplied: the round trip of
+      // a buffer (MMAs, commit, the epilogue's wake-up and reads, its arrive)
+      // is some 1200 cycles against the 1024 of two blocks' MMAs; as one
+      // 256-column buffer a block it was 1500, and that set the pace.
+      // Warp 3 does the waiting, half by half and one half ahead, and the two
+      // meet at a named barrier: an mbarrier test takes some 85 cycles to
+      // answer, and with two of them a half this warp's own instructions were
+      // the bound (900 cycles a block).  Where warp 3 has given up, it only
+      // passes: the MMAs then work on what is there, and the status is set.
+      const uint64_t rd0 = make_sdesc_sw128(smem_u32(smem)), wd0 = make_sdesc_sw128(smem_u32(smem + kFp8WBytes));
+      const uint32_t d_bar = smem_u32(d_full), e_bar = smem_u32(empty);
       int s = 0, b = 0;
-      bool ok = true, tried = false, have_rows = false, have_d = false;
-      for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x) {
-        for (int kb = 0; kb < nk; ++kb, ++i) {
-          if (!tried || !have_rows) ok = ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, u);
-          if (!tried || !have_d) ok = ok && ab.wait(&d_empty[b], ((i / DB) & 1) ^ 1, kTagDEmpty, i, u);
-          if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t rd = make_sdesc_sw128(smem_u32(smem + s * kFp8TileStageBytes));
-            const uint64_t wd = make_sdesc_sw128(smem_u32(smem + s * kFp8TileStageBytes + kFp8WBytes));
+      bool issued = false;
+      for (int u = u0; u < n_units; u += du) {
+        for (int kb = 0; kb < nk; ++kb) {
+          const uint64_t rd = rd0 + s * (Cfg::kStageBytes >> 4), wd = wd0 + s * (Cfg::kStageBytes >> 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma_ss_f8(tmem + b * 256, rd + 2 * j, wd + 2 * j, idesc, j > 0);
-            mma_commit(&d_full[b]);
-            mma_commit(&empty[s]);
+          for (int h = 0; h < 2; ++h) {
+            named_bar_sync(kBarHandoff, 64);
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                Pair::mma(tmem + b * 256 + h * 128, rd + 2 * j, wd + h * (Cfg::kWRows * 128 / 2 >> 4) + 2 * j, j > 0);
+              Pair::commit(d_bar + 8 * (2 * b + h));
+              if (h == 1) Pair::commit(e_bar + 8 * s);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          issued = true;
           if (++s == NST) s = 0;
           b ^= 1;
-          have_rows = mbar_test_wait(&full[s], ((i + 1) / NST) & 1);
-          have_d = mbar_test_wait(&d_empty[b], (((i + 1) / DB) & 1) ^ 1);
-          tried = true;
         }
       }
-      if (i > 0) {   // drain
-        if (elect_one()) mma_commit(drain_bar);
+      if (issued) {   // drain
+        if (elect_one()) Pair::commit(smem_u32(drain_bar));
         __syncwarp();
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain_bar, 0) && globaltimer_ns() - t0 < 1000000000ull) {}
       }
+    } else if (warp == 3 && rank == 0) {
+      // ------------------------------------------- the MMAs' waits ---
+      uint32_t i = 0;
+      int s = 0, phase = 0;
+      bool ok = true;
+      for (int u = u0; u < n_units; u += du) {
+        for (int kb = 0; kb < nk; ++kb, ++i) {
+          const uint32_t b = i & 1, dp = ((i >> 1) & 1) ^ 1;
+          ok = ok && ab.wait(&full[s], phase, kTagWFull, i, u);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && ab.wait(&d_empty[2 * b + h], dp, kTagDEmpty, i, u);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            named_bar_sync(kBarHandoff, 64);
+          }
+          if (++s == NST) { s = 0; phase ^= 1; }
+        }
+      }
+    } else if (warp == 2 && NMAT == 1) {
+      // -------------------------------------------- output stores ---
+      // The staged features of each half (128 bf16; or 64 fp32, twice), as
+      // 32-row boxes of 128 bytes, behind the next tile's sums: stores from the
+      // epilogue warps themselves held them, and with them the MMAs, for a
+      // quarter of the time.  A box that would reach past the group's rows, and
+      // an output without a tensor map, goes by plain stores.
+      const bool f32 = p.out_type == FT_F32;
+      const int esize = f32 ? 4 : 2, per = 128 / esize;   // features a chunk
+      uint32_t n = 0;
+      bool ok = true;
+      for (int u = u0; u < n_units && ok; u += du) {
+        const Fp8Unit d = fp8_unit(p, u, Cfg::kRows);
+        const int rb = d.rb + rank * 128, nr = max(0, min(d.nr - int(rank) * 128, 128));
+        for (int pass = 0; pass < (f32 ? 2 : 1) && ok; ++pass, ++n) {
+          for (int half = 0; half < 2; ++half) {
+            if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&out_full[half], n & 1, kTagOut, n, u)))) break;
+            for (int c = 0; c < 2; ++c) {
+              const uint8_t* stage = out_stage + (half * 2 + c) * kFp8OutChunk;
+              const int f0 = d.ft * 256 + half * 128 + (2 * pass + c) * per, nf = min(per, p.N - f0);
+              const int boxes = p.out_tma ? nr / 32 : 0;
+              if (nf <= 0) break;
+              if (lane < boxes) tma_store_2d(&tm_out, stage + lane * 32 * 128, f0, rb + lane * 32);
+              for (int row = boxes * 32 + (lane >> 3); row < nr; row += 4) {
+                const int piece = lane & 7;
+                const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                const int f = piece * (16 / esize);
+                uint8_t* dst = static_cast<uint8_t*>(p.out) + ((rb + row) * p.ldo + f0 + f) * esize;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  if (f32) {
+                    if (e < 4 && f + e < nf) reinterpret_cast<uint32_t*>(dst)[e] = w[e & 3];
+                  } else if (f + e < nf) {
+                    reinterpret_cast<uint16_t*>(dst)[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
+                  }
+                }
+              }
+            }
+            asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read 0;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&out_empty[half]);
+          }
+        }
+      }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // -------------------------------------------------- epilogue ---
     const int quarter = warp & 3, half = (warp - 4) >> 2;
-    const int row = quarter * 32 + lane;                 // token row within the tile = tensor-memory lane
+    const int row = quarter * 32 + lane;                 // token row within the CTA's 128 = tensor-memory lane
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
+    uint32_t d_empty_addr[DB];
+#pragma unroll
+    for (int b = 0; b < DB; ++b) d_empty_addr[b] = PAIR ? cluster_addr(&d_empty[2 * b + half], 0) : 0;
     EpiSync epi{epi_bar, ab, 0};
-    uint32_t i = 0;
+    uint32_t i = 0, staged = 0;
     bool ok = true;
     int parity = 0;
-    for (int u = blockIdx.x; u < n_units && ok; u += gridDim.x, parity ^= 1) {
-      const Fp8Unit d = fp8_unit(p, u, 128);
-      const bool live = row < d.nr;
-      const float* sr = p.sa + (long long)(d.rb + (live ? row : 0)) * p.ld_sa;
+    // A tile's descriptor and its first two blocks' scales are fetched behind
+    // the tile before it: two dependent round trips to memory.
+    Fp8Unit d = {};
+    const float *sr, *sw0, *sw1;
+    float a, w0, w1, an, w0n, w1n;
+    const int last = nk - 1;
+    auto fetch_scales = [&]() {
+      sr = p.sa + (long long)(int(rank) * 128 + row < d.nr ? d.rb + int(rank) * 128 + row : d.rb) * p.ld_sa;
       // a feature block past the end has no scales: its columns are zeros, and block 0's scale does
       const int block = NMAT == 2 ? d.ft : d.ft * 2 + half;
-      const bool has = block * kFp8Block < p.N;
-      const float* sw0 = fp8_weight_scales(p, 0, d.slot, has ? block : 0);
-      const float* sw1 = NMAT == 2 ? fp8_weight_scales(p, 1, d.slot, block) : sw0;
+      sw0 = fp8_weight_scales(p, 0, d.slot, block * kFp8Block < p.N ? block : 0);
+      sw1 = NMAT == 2 ? fp8_weight_scales(p, 1, d.slot, block) : sw0;
+      const int k1 = min(1, last);
+      a = __ldg(sr);
+      w0 = __ldg(sw0);
+      w1 = NMAT == 2 ? __ldg(sw1) : 0.0f;
+      an = __ldg(sr + k1);
+      w0n = __ldg(sw0 + k1);
+      w1n = NMAT == 2 ? __ldg(sw1 + k1) : 0.0f;
+    };
+    if (u0 < n_units) {
+      d = fp8_unit(p, u0, Cfg::kRows);
+      fetch_scales();
+    }
+    for (int u = u0; u < n_units && ok; u += du, parity ^= 1) {
+      const int rb = d.rb + rank * 128;
+      const bool live = int(rank) * 128 + row < d.nr;
       unsigned long long acc[64];   // NMAT 1: 128 columns; NMAT 2: gate of 64 features, then up
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = 0ull;
-      float a = __ldg(sr), w0 = __ldg(sw0), w1 = NMAT == 2 ? __ldg(sw1) : 0.0f;
       // Chunks of 32 columns in two register buffers, the next chunk's load in
       // flight behind one chunk's sums -- also across blocks: the last chunk's
       // sums stand behind the next block's first load.
       uint32_t v[2][32];
-      if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[i & 1], (i >> 1) & 1, kTagDFull, i, u)))) break;
+      if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[2 * (i & 1) + half], (i >> 1) & 1, kTagDFull, i, u)))) break;
       tc_fence_after();
       const uint32_t dcol = tmem + lane_base + half * 128;
       tmem_ld_32x32b_x32(dcol + (i & 1) * 256, v[0]);
       for (int kb = 0; kb < nk; ++kb, ++i) {
         const uint32_t b = i & 1;
         const float s0 = a * w0, s1 = a * w1;
-        const unsigned long long p0 = pack2(__float_as_uint(s0), __float_as_uint(s0));
-        const unsigned long long p1 = NMAT == 2 ? pack2(__float_as_uint(s1), __float_as_uint(s1)) : p0;
-        const bool more = kb + 1 < nk;
-        if (more) {
-          a = __ldg(++sr);
-          w0 = __ldg(++sw0);
-          if (NMAT == 2) w1 = __ldg(++sw1);
-        }
+        const unsigned long long p0 = pack2(s0, s0);
+        const unsigned long long p1 = NMAT == 2 ? pack2(s1, s1) : p0;
+        a = an;
+        w0 = w0n;
+        w1 = w1n;
+        const int k2 = min(kb + 2, last);
+        an = __ldg(sr + k2);
+        w0n = __ldg(sw0 + k2);
+        if (NMAT == 2) w1n = __ldg(sw1 + k2);
         bool ready = false;
+        auto sums = [&](int c) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+          for (int n = 0; n < 16; ++n) fma2_to(acc[c * 16 + n], v[c & 1][2 * n], v[c & 1][2 * n + 1], c < 2 ? p0 : p1);
+        };
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
           tmem_wait_ld();
-          if (c < 3) {
-            tmem_ld_32x32b_x32(dcol + b * 256 + (c + 1) * 32, v[(c + 1) & 1]);
-            if (c == 1) ready = mbar_test_wait(&d_full[b ^ 1], ((i + 1) >> 1) & 1);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[b]);
-            if (more) {
-              if (!ready) ok = ab.wait(&d_full[b ^ 1], ((i + 1) >> 1) & 1, kTagDFull, i + 1, u);
-              if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-              tc_fence_after();
-              tmem_ld_32x32b_x32(dcol + (b ^ 1) * 256, v[0]);
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < 16; ++n) fma2(acc[c * 16 + n], pack2(v[c & 1][2 * n], v[c & 1][2 * n + 1]), c < 2 ? p0 : p1);
+          tmem_ld_32x32b_x32(dcol + b * 256 + (c + 1) * 32, v[(c + 1) & 1]);
+          if (c == 2) ready = mbar_test_wait(&d_full[2 * (b ^ 1) + half], ((i + 1) >> 1) & 1);
+          sums(c);
         }
-        if (!ok) break;
+        tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_cluster(b ? d_empty_addr[1] : d_empty_addr[0]);
+          else mbar_arrive(&d_empty[2 * b + half]);
+        }
+        if (kb == last) {
+          sums(3);
+        } else {
+          if (!ready) {
+            sums(3);
+            if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[2 * (b ^ 1) + half], ((i + 1) >> 1) & 1, kTagDFull, i + 1, u))))
+              break;
+          }
+          tc_fence_after();
+          tmem_ld_32x32b_x32(dcol + (b ^ 1) * 256, v[0]);
+          if (ready) sums(3);
+        }
       }
       if (!ok) break;
+      const int ft = d.ft;
+      if (u + du < n_units) d = fp8_unit(p, u + du, Cfg::kRows);
       if constexpr (NMAT == 1) {
-        // Through 4 KB of shared memory a warp, 64 bf16 or 32 fp32 columns of its
-        // 32 rows at a time: a thread has a row's columns, but stores of whole
-        // 128-byte rows, four rows an instruction, are what the memory takes
-        // well (16-byte stores to 32 rows took half of the unit's time).
-        uint8_t* stage = out_stage + (warp - 4) * 4096;
-        const int f0 = d.ft * 256 + half * 128;
-        const int esize = p.out_type == FT_F32 ? 4 : 2;
-        const bool vec = (p.ldo * esize) % 16 == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0;
+        // each thread its row's features, to the store warp: 16-byte piece q of a row at q ^ (row % 8)
+        uint8_t* stage = out_stage + half * 2 * kFp8OutChunk + row * 128;
+        const bool f32 = p.out_type == FT_F32;
 #pragma unroll
-        for (int c0 = 0; c0 < 128; c0 += 32) {
-          // 16-byte piece q of the thread's row at q ^ (row % 8)
-          const bool f32 = p.out_type == FT_F32;
-          if (f32) {
+        for (int pass = 0; pass < 2; ++pass) {
+          if (pass == 1 && !f32) break;
+          if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&out_empty[half], (staged & 1) ^ 1, kTagOut, staged, u)))) break;
+          ++staged;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float2 x = unpack2(acc[c0 / 2 + 2 * q]), y = unpack2(acc[c0 / 2 + 2 * q + 1]);
-              *reinterpret_cast<float4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_float4(x.x, x.y, y.x, y.y);
-            }
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t o[4];
+          for (int q = 0; q < 16; ++q) {
+            uint32_t o[4];
+            if (f32) {
+              const float2 x = unpack2(acc[pass * 32 + 2 * q]), y = unpack2(acc[pass * 32 + 2 * q + 1]);
+              o[0] = __float_as_uint(x.x); o[1] = __float_as_uint(x.y);
+              o[2] = __float_as_uint(y.x); o[3] = __float_as_uint(y.y);
+            } else {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float2 x = unpack2(acc[c0 / 2 + 4 * q + e]);
+                const float2 x = unpack2(acc[4 * q + e]);
                 const __nv_bfloat162 t = __floats2bfloat162_rn(x.x, x.y);
                 o[e] = *reinterpret_cast<const uint32_t*>(&t);
               }
-              const int piece = (c0 & 32) / 8 + q;
-              *reinterpret_cast<uint4*>(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
             }
-            if (!(c0 & 32)) continue;
+            *reinterpret_cast<uint4*>(stage + (q >> 3) * kFp8OutChunk + (((q & 7) ^ (row & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
           }
+          fence_proxy_async_smem();
           __syncwarp();
-          const int fc = f0 + (f32 ? c0 : c0 - 32);   // the chunk's first feature
-#pragma unroll
-          for (int r = 0; r < 32; r += 4) {
-            const int rr = r + (lane >> 3), piece = lane & 7;
-            const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
-            const int tile_row = quarter * 32 + rr, f = fc + piece * (16 / esize);
-            if (tile_row >= d.nr || f >= p.N) continue;
-            uint8_t* dst = static_cast<uint8_t*>(p.out) + ((d.rb + tile_row) * p.ldo + f) * esize;
-            if (vec && f + 16 / esize <= p.N) {
-              *reinterpret_cast<uint4*>(dst) = x;
-            } else {
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                if (f32) {
-                  if (e < 4 && f + e < p.N) reinterpret_cast<uint32_t*>(dst)[e] = w[e & 3];
-                } else if (f + e < p.N) {
-                  reinterpret_cast<uint16_t*>(dst)[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
-                }
-              }
-            }
-          }
-          __syncwarp();
+          if (lane == 0) mbar_arrive(&out_full[half]);
         }
+        fetch_scales();
+        if (!ok) break;
       } else {
         // h of this thread's 64 features; its scale is the maximum over the row's 128 (those past N are zeros)
-        float h[64];
-        uint32_t m = 0;
+        float h[64], hm = 0.0f;
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           const float2 g = unpack2(acc[c]), up = unpack2(acc[32 + c]);
           h[2 * c] = fp8_silu_mul(g.x, up.x);
           h[2 * c + 1] = fp8_silu_mul(g.y, up.y);
-          m = max(m, max(abs_bits(h[2 * c]), abs_bits(h[2 * c + 1])));
+          hm = fmaxf(hm, fmaxf(fabsf(h[2 * c]), fabsf(h[2 * c + 1])));   // leaves NaN out
         }
+        uint32_t m = __float_as_uint(hm);
         tmax[parity * 256 + half * 128 + row] = m;
+        fetch_scales();
         if (!(ok = epi.sync(lane))) break;
         m = max(m, tmax[parity * 256 + (half ^ 1) * 128 + row]);
         const Fp8Scale f = fp8_scale_of(__uint_as_float(m));
         const float inv = fp8_factor_of(f);
-        const int f0 = d.ft * 128 + half * 64;
+        const int f0 = ft * 128 + half * 64;
         if (live) {
-          if (half == 0) p.hs[(long long)(d.rb + row) * ((p.N + kFp8Block - 1) / kFp8Block) + d.ft] = f.scale;
+          if (half == 0) p.hs[(long long)(rb + row) * ((p.N + kFp8Block - 1) / kFp8Block) + ft] = f.scale;
           if (f0 < p.N) {   // N is a multiple of 64
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (d.rb + row) * p.ldo + f0);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (rb + row) * p.ldo + f0);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               uint32_t o[4];
@@ -689,10 +867,11 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   }
   tc_fence_before();
   __syncthreads();
+  if (PAIR) cluster_sync();   // neither CTA leaves while the other may still signal it
   pdl_launch_dependents();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    Pair::dealloc(tmem);
   }
 }
 
@@ -705,7 +884,7 @@ __global__ void __launch_bounds__(256) fp8_zero_kernel(int* counters, int n) {
 
 // One launch: blocks [0, sched.nsched) build the two work lists and clear the
 // counters (prep_schedule of ffn.cu), the others write the token rows in FP8
-// in permuted order, sixteen lanes a group of 128 values.
+// in permuted order, eight lanes a group of 128 values.
 struct Fp8PrepParams {
   PrepParams sched;
   const __nv_bfloat16* x;
@@ -719,28 +898,38 @@ __global__ void __launch_bounds__(256) fp8_prep_kernel(const Fp8PrepParams p) {
     prep_schedule(p.sched, blockIdx.x);
     return;
   }
-  const int H = p.sched.H, nb = (H + kFp8Block - 1) / kFp8Block;
-  const long long g = ((long long)(blockIdx.x - p.sched.nsched) * blockDim.x + threadIdx.x) >> 4;
-  const bool live = g < (long long)p.sched.P * nb;
-  const int sub = threadIdx.x & 15;
-  const int r = live ? int(g / nb) : 0;
-  const int b = live ? int(g - (long long)r * nb) : 0;
-  const int src = __ldg(p.sched.perm_src + r);
-  const int t = src / p.sched.k_top;
-  const bool known = src >= 0 && t < p.T;
-  if (live && !known && b == 0 && sub == 0) set_device_status(FT_DEV_BAD_INDEX);
-  const int k0 = b * kFp8Block + sub * 8;
-  float v[8];
-  load8<__nv_bfloat16, true>(p.x + (long long)(known ? t : 0) * H + k0, live && known ? min(8, H - k0) : 0, v);
-  float m = absmax8(v);
-#pragma unroll
-  for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
-  if (!live) return;
-  const Fp8Scale f = fp8_scale_of(m);
-  if (sub == 0) p.scales[(long long)r * nb + b] = f.scale;
-  if (k0 < H)   // H is a multiple of 64
-    *reinterpret_cast<uint2*>(p.codes + (long long)r * H + k0) =
-        make_uint2(fp8_codes4(v[0], v[1], v[2], v[3], f), fp8_codes4(v[4], v[5], v[6], v[7], f));
+  const int H = p.sched.H;
+  const uint32_t nb = (H + kFp8Block - 1) / kFp8Block, groups = uint32_t(p.sched.P) * nb;   // T k <= 2^24, nb <= 512
+  const uint32_t block = blockIdx.x - p.sched.nsched, stride = (gridDim.x - p.sched.nsched) * 32u;
+  const int sub = threadIdx.x & 7;
+  Raw16<__nv_bfloat16> raw;
+  uint32_t r = 0, b = 0;
+  auto fetch = [&](uint32_t g) {
+    r = g / nb;
+    b = g - r * nb;
+    const bool live = g < groups;
+    const int src = live ? __ldg(p.sched.perm_src + r) : -1, t = src / p.sched.k_top;
+    const bool known = src >= 0 && t < p.T;
+    if (live && !known && b == 0 && sub == 0) set_device_status(FT_DEV_BAD_INDEX);
+    const int k0 = b * kFp8Block + sub * 16;   // H is a multiple of 64: all sixteen or none
+    if (known && k0 < H) raw.load(p.x + (long long)t * H + k0);
+    else raw.zero();
+  };
+  uint32_t g = (block * 256u + threadIdx.x) >> 3;
+  fetch(g);
+  for (uint32_t w = (block * 256u + (threadIdx.x & ~31u)) >> 3; w < groups; w += stride) {
+    float v[16];
+    raw.to(v);
+    const uint32_t row = r, c = b;
+    const bool live = g < groups;
+    g += stride;
+    if (w + stride < groups) fetch(g);
+    const Fp8Scale f = fp8_scale_of(group_max(v));
+    if (!live) continue;
+    if (sub == 0) p.scales[(long long)row * nb + c] = f.scale;
+    const int k0 = c * kFp8Block + sub * 16;
+    if (k0 < H) *reinterpret_cast<uint4*>(p.codes + (long long)row * H + k0) = fp8_codes16(v, f);
+  }
 }
 
 // ---------------------------------------------------------------- host ---
@@ -759,10 +948,25 @@ static bool make_fp8_map(const void* base, long long rows, int K, long long pitc
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch with the kernel's dynamic shared memory allowed on the current device.
+// The output [rows, N] as boxes of 32 rows x 128 bytes; false where its pitch or address does not allow a map.
+static bool make_fp8_out_map(void* out, int out_type, long long rows, int N, long long ldo, CUtensorMap* m) {
+  auto enc = tensor_map_encoder();
+  const int esize = out_type == FT_F32 ? 4 : 2;
+  if (!enc || (ldo * esize) % 16 || (reinterpret_cast<uintptr_t>(out) & 15)) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(N), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(ldo * esize)};
+  const cuuint32_t box[2] = {cuuint32_t(128 / esize), 32};
+  const cuuint32_t es[2] = {1, 1};
+  return enc(m, out_type == FT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims,
+             strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launch with the kernel's dynamic shared memory allowed on the current
+// device, in clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_fp8(void (*kern)(KArgs...), int grid, int threads, int smem, std::atomic<uint64_t>& done,
-                              cudaStream_t s, Args&&... args) {
+static cudaError_t launch_fp8(void (*kern)(KArgs...), int grid, int threads, int smem, int cluster,
+                              std::atomic<uint64_t>& done, cudaStream_t s, Args&&... args) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -771,34 +975,75 @@ static cudaError_t launch_fp8(void (*kern)(KArgs...), int grid, int threads, int
     if (e != cudaSuccess) return e;
     if (dev < 64) done.fetch_or(uint64_t(1) << dev);
   }
-  return launch_pdl(kern, dim3(grid), dim3(threads), smem, s, std::forward<Args>(args)...);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 template <int NMAT, int BN>
 static cudaError_t launch_fp8_stream(const Fp8Params& p, int grid, const CUtensorMap& w0, const CUtensorMap& w1,
                                      const CUtensorMap& rows, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  return launch_fp8(fp8_stream_kernel<NMAT, BN>, grid, kFp8StreamThreads, Fp8StreamCfg<NMAT, BN>::kSmemBytes, done, s, p,
-                    w0, w1, rows);
+  return launch_fp8(fp8_stream_kernel<NMAT, BN>, grid, kFp8StreamThreads, Fp8StreamCfg<NMAT, BN>::kSmemBytes, 1, done, s,
+                    p, w0, w1, rows);
 }
-template <int NMAT>
+template <int NMAT, bool PAIR>
 static cudaError_t launch_fp8_tile(const Fp8Params& p, int grid, const CUtensorMap& w0, const CUtensorMap& w1,
-                                   const CUtensorMap& rows, cudaStream_t s) {
+                                   const CUtensorMap& rows, const CUtensorMap& out, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  return launch_fp8(fp8_tile_kernel<NMAT>, grid, kFp8TileThreads, kFp8TileSmemBytes, done, s, p, w0, w1, rows);
+  return launch_fp8(fp8_tile_kernel<NMAT, PAIR>, grid, kFp8TileThreads, Fp8TileCfg<NMAT, PAIR>::kSmemBytes, PAIR ? 2 : 1, done,
+                    s, p, w0, w1, rows, out);
 }
 template <int NMAT>
-static cudaError_t launch_fp8_any(int bn, const Fp8Params& p, int grid, const CUtensorMap& w0, const CUtensorMap& w1,
-                                  const CUtensorMap& rows, cudaStream_t s) {
+static cudaError_t launch_fp8_any(int bn, Fp8Params p, long long out_rows, int grid, const CUtensorMap& w0,
+                                  const CUtensorMap& w1, const CUtensorMap& rows, cudaStream_t s) {
+  CUtensorMap out = rows;
+  if (bn >= 128 && NMAT == 1) p.out_tma = make_fp8_out_map(p.out, p.out_type, out_rows, p.N, p.ldo, &out);
   switch (bn) {
     case 16: return launch_fp8_stream<NMAT, 16>(p, grid, w0, w1, rows, s);
     case 32: return launch_fp8_stream<NMAT, 32>(p, grid, w0, w1, rows, s);
     case 64: return launch_fp8_stream<NMAT, 64>(p, grid, w0, w1, rows, s);
-    default: return launch_fp8_tile<NMAT>(p, grid, w0, w1, rows, s);
+    case 128: return launch_fp8_tile<NMAT, false>(p, grid, w0, w1, rows, out, s);
+    default: return launch_fp8_tile<NMAT, true>(p, grid, w0, w1, rows, out, s);
   }
 }
 
-// Token rows a tile takes (16, 32, 64: the stream kernel; 128: the tile kernel).
-static int fp8_rows_tile(double rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+// Rows, padded to tiles of b, of a group of `mean` rows that spread by their square root.
+static double fp8_padded(double mean, int b) {
+  double sum = 0.0;
+  for (double q : {-1.4, -0.7, -0.3, 0.0, 0.3, 0.7, 1.4}) sum += b * ceil(std::max(1.0, mean + q * sqrt(mean)) / b) / 7;
+  return sum;
+}
+// Token rows a tile takes (16, 32, 64: the stream kernel; 128, 256: the tile
+// kernel on one CTA or a pair).  For few rows a quarter more than the mean, so
+// that most groups of an even spread are one tile.  A pair takes 0.9 of the
+// time for the same padded rows (32 groups of some 187 rows, two or one tile
+// each: the FFN 241 us against 270) but pads more (4096 skewed tokens of
+// 128 groups: 316 us against 277).
+static int fp8_rows_tile(double mean) {
+  const double rows = 1.25 * mean;
+  if (rows <= 64) return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  return 0.9 * fp8_padded(mean, 256) < fp8_padded(mean, 128) ? 256 : 128;
+}
+// Rows of a token box, and of a weight box of `nmat` matrices.
+static int fp8_row_box(int bn) { return std::min(bn, 128); }
+static int fp8_weight_box(int bn, int nmat) {
+  return bn < 128 ? 128 : bn == 128 ? (nmat == 2 ? 64 : 256) : (nmat == 2 ? 128 : 64);
+}
+
+static int fp8_tile_grid(long long units, int bn, int num_sms) {
+  return bn == 256 ? 2 * int(std::min<long long>(units, num_sms / 2)) : int(std::min<long long>(units, num_sms));
+}
 
 struct Fp8GemmPlan {
   int bn, row_tiles, feat_tiles, grid, min_blocks;
@@ -809,13 +1054,13 @@ static Fp8GemmPlan plan_fp8_gemm(int M, int N, int K, int num_sms) {
   Fp8GemmPlan pl{};
   const int nk = fp8_blocks(K);
   const long long big = ((M + 127LL) / 128) * ((N + 255LL) / 256);
-  pl.bn = M <= 64 ? fp8_rows_tile(M) : big * 2 >= num_sms ? 128 : 64;
+  pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || big * 2 < num_sms ? 64 : M > 512 ? 256 : 128;
   pl.row_tiles = (M + pl.bn - 1) / pl.bn;
-  pl.feat_tiles = pl.bn == 128 ? (N + 255) / 256 : (N + 127) / 128;
+  pl.feat_tiles = pl.bn >= 128 ? (N + 255) / 256 : (N + 127) / 128;
   const long long units = (long long)pl.row_tiles * pl.feat_tiles;
   pl.min_blocks = 1;
-  if (pl.bn == 128) {
-    pl.grid = int(std::min<long long>(units, num_sms));
+  if (pl.bn >= 128) {
+    pl.grid = fp8_tile_grid(units, pl.bn, num_sms);
     return pl;
   }
   const long long per = std::max<long long>((units * nk + num_sms - 1) / num_sms, pl.min_blocks);
@@ -834,8 +1079,8 @@ static cudaError_t launch_fp8_gemm(const uint8_t* a, long long lda, const float*
                                    int out_type, long long ldo, void* ws, cudaStream_t s, const char** why) {
   const Fp8GemmPlan pl = plan_fp8_gemm(M, N, K, device_sm_count());
   CUtensorMap tm_a, tm_b;
-  if (!make_fp8_map(a, M, K, lda, 1, 16, pl.bn, false, &tm_a) ||
-      !make_fp8_map(b, N, K, ldb, 1, ldb * N, pl.bn == 128 ? 256 : 128, true, &tm_b)) {
+  if (!make_fp8_map(a, M, K, lda, 1, 16, fp8_row_box(pl.bn), false, &tm_a) ||
+      !make_fp8_map(b, N, K, ldb, 1, ldb * N, fp8_weight_box(pl.bn, 1), true, &tm_b)) {
     *why = "ft_fp8_gemm: cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
   }
@@ -862,7 +1107,7 @@ static cudaError_t launch_fp8_gemm(const uint8_t* a, long long lda, const float*
     if (e != cudaSuccess) return e;
   }
   ProfileScope prof(FT_KERNEL_FP8_GEMM, s);
-  return launch_fp8_any<1>(pl.bn, p, pl.grid, tm_b, tm_b, tm_a, s);
+  return launch_fp8_any<1>(pl.bn, p, M, pl.grid, tm_b, tm_b, tm_a, s);
 }
 
 struct Fp8FfnPlan {
@@ -876,16 +1121,15 @@ static Fp8FfnPlan plan_fp8_ffn(int T, int H, int I, int E, int k) {
   const int num_sms = device_sm_count();
   const long long P = (long long)T * k;
   const double distinct = E * (1.0 - pow(1.0 - double(k) / E, double(T)));
-  // a quarter more than the mean, so that most groups of an even spread are one tile
-  p.bn = fp8_rows_tile(1.25 * double(P) / std::max(distinct, 1.0));
+  p.bn = fp8_rows_tile(double(P) / std::max(distinct, 1.0));
   p.mt1 = fp8_blocks(I);
-  p.mt2 = p.bn == 128 ? (H + 255) / 256 : fp8_blocks(H);
+  p.mt2 = p.bn >= 128 ? (H + 255) / 256 : fp8_blocks(H);
   const long long tiles = std::min<long long>(E, P) + P / p.bn;
   p.max_units1 = tiles * p.mt1;
   p.max_units2 = tiles * p.mt2;
   const bool stream = p.bn < 128;
-  p.grid1 = stream ? num_sms : int(std::min<long long>(num_sms, p.max_units1));
-  p.grid2 = stream ? num_sms : int(std::min<long long>(num_sms, p.max_units2));
+  p.grid1 = stream ? num_sms : fp8_tile_grid(p.max_units1, p.bn, num_sms);
+  p.grid2 = stream ? num_sms : fp8_tile_grid(p.max_units2, p.bn, num_sms);
   size_t o = 0;
   p.off_x = o;      o = align256(o + size_t(P) * H);
   p.off_xs = o;     o = align256(o + size_t(P) * fp8_blocks(H) * 4);
@@ -912,11 +1156,11 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
   const bool stream = pl.bn < 128;
   CUtensorMap tm[3], tm_x, tm_h;
   const int rows[3] = {I, I, H}, Ks[3] = {H, H, I};
-  bool ok = make_fp8_map(w + pl.off_x, P, H, H, 1, 16, pl.bn, false, &tm_x) &&
-            make_fp8_map(w + pl.off_h, P, I, I, 1, 16, pl.bn, false, &tm_h);
+  bool ok = make_fp8_map(w + pl.off_x, P, H, H, 1, 16, fp8_row_box(pl.bn), false, &tm_x) &&
+            make_fp8_map(w + pl.off_h, P, I, I, 1, 16, fp8_row_box(pl.bn), false, &tm_h);
   for (int m = 0; m < 3; ++m)
     ok = ok && make_fp8_map(pool + L.codes_off[m], rows[m], Ks[m], Ks[m], L.num_slots, L.slot_bytes,
-                            stream ? 128 : m == FT_DOWN ? 256 : 64, true, &tm[m]);
+                            fp8_weight_box(pl.bn, m == FT_DOWN ? 1 : 2), true, &tm[m]);
   if (!ok) {
     *why = "ft_moe_ffn_fp8: cuTensorMapEncodeTiled failed";
     return cudaErrorInvalidValue;
@@ -952,9 +1196,9 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
     pp.T = T;
     pp.codes = w + pl.off_x;
     pp.scales = reinterpret_cast<float*>(w + pl.off_xs);
-    const long long threads = 16LL * P * fp8_blocks(H);
+    const long long groups = (long long)P * fp8_blocks(H);
     ProfileScope prof(FT_KERNEL_PREP, s);
-    e = launch_pdl(fp8_prep_kernel, dim3(unsigned(sp.nsched + (threads + 255) / 256)), dim3(256), 0, s, pp);
+    e = launch_pdl(fp8_prep_kernel, dim3(sp.nsched + fp8_quant_grid(groups, device_sm_count())), dim3(256), 0, s, pp);
   }
   if (e != cudaSuccess) return e;
   Fp8Params p{};
@@ -975,7 +1219,7 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
   p.min_blocks = 1;
   {
     ProfileScope prof(FT_KERNEL_FP8_GATE_UP, s);
-    e = launch_fp8_any<2>(pl.bn, p, pl.grid1, tm[FT_GATE], tm[FT_UP], tm_x, s);
+    e = launch_fp8_any<2>(pl.bn, p, P, pl.grid1, tm[FT_GATE], tm[FT_UP], tm_x, s);
   }
   if (e != cudaSuccess) return e;
   p.sa = reinterpret_cast<const float*>(w + pl.off_hs);
@@ -991,7 +1235,7 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
   p.ldo = H;
   p.counters = reinterpret_cast<int*>(w + pl.off_cnt2);
   ProfileScope prof(FT_KERNEL_FP8_DOWN, s);
-  return launch_fp8_any<1>(pl.bn, p, pl.grid2, tm[FT_DOWN], tm[FT_DOWN], tm_h, s);
+  return launch_fp8_any<1>(pl.bn, p, P, pl.grid2, tm[FT_DOWN], tm[FT_DOWN], tm_h, s);
 }
 
 }  // namespace ftmoe

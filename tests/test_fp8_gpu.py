@@ -122,7 +122,8 @@ def _check_product(out, a, b):
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 1), (1, 2048, 2048), (2, 100, 130), (7, 257, 64), (8, 128, 128), (16, 130, 1100), (17, 384, 2880),
     (33, 1000, 15), (64, 2880, 2880), (65, 129, 257), (128, 256, 512), (129, 300, 700), (200, 1234, 1100),
-    (300, 512, 127), (1, 7, 4096), (1037, 1234, 1100), (260, 5000, 96), (2, 20000, 64)])
+    (300, 512, 127), (1, 7, 4096), (1037, 1234, 1100), (260, 5000, 96), (2, 20000, 64),
+    (300, 6500, 200), (1100, 2500, 300), (600, 4104, 130), (513, 7001, 1030)])
 def test_gemm(M, N, K, out):
     a, b = _operands(M, N, K, M * 7 + N * 3 + K)
     y = fp8.Fp8Linear(*b).matmul(*a, out_dtype=DTYPES[out])
@@ -260,7 +261,7 @@ class Ffn:
 FFN_SHAPES = [
     ([1], 256, 256, 1), ([0, 1, 0], 256, 512, 1), ([2, 0, 5, 1], 320, 448, 2), ([16, 17, 1, 30], 256, 512, 2),
     ([64, 65, 3], 512, 320, 3), ([128], 256, 256, 1), ([129, 0, 127], 320, 256, 2), ([300, 1, 210], 256, 576, 1),
-    ([700, 0], 512, 256, 2), ([1, 1, 1, 1, 1, 1, 1, 1], 2048, 768, 8), ([3, 2], 2880, 2880, 1), ([90, 160], 576, 2880, 2)]
+    ([700, 0], 512, 256, 2), ([257, 255, 100, 513], 320, 448, 3), ([140, 90, 130], 256, 512, 1), ([1, 1, 1, 1, 1, 1, 1, 1], 2048, 768, 8), ([3, 2], 2880, 2880, 1), ([90, 160], 576, 2880, 2)]
 
 
 @pytest.mark.parametrize("out", ["fp32", "bf16"])
