@@ -426,13 +426,11 @@ FT_API int ft_fp8_pack(const float* w, int N, int K, uint8_t* codes, int64_t ld_
  *   sa        device fp32 [M, ceil(K/128)], row pitch ld_sa elements
  *   sb        device fp32 [ceil(N/128), ceil(K/128)], row pitch ld_sb elements
  *   out       device [M, N] of type out_type (FT_F32 or FT_BF16), row pitch ldo elements (out)
- *   ws        device workspace of ft_fp8_gemm_workspace_size bytes, 256-byte aligned; no zeroing
- * Any M, N, K from 1 up (K < 2^24); no alignment of M, N or K is needed.  M = 0 is a no-op.
+ * Any M, N, K from 1 up (K < 2^24); no alignment of M, N or K is needed.  M = 0 is a no-op.  No workspace.
  */
 FT_API int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64_t ld_sa, const uint8_t* b,
                        int64_t ldb, const float* sb, int64_t ld_sb, int M, int N, int K, void* out, int out_type,
-                       int64_t ldo, void* ws, size_t ws_bytes, ft_stream_t stream);
-FT_API size_t ft_fp8_gemm_workspace_size(int M, int N, int K);
+                       int64_t ldo, ft_stream_t stream);
 
 /*
  * ft_moe_ffn_nvfp4 over FP8 experts.  For row r of group e (token

@@ -96,8 +96,7 @@ _SIGS = {
                                   c_void_p]),
     "ft_fp8_pack": (c_int, [c_void_p, c_int, c_int, c_void_p, c_int64, c_void_p, c_int, c_void_p]),
     "ft_fp8_gemm": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int, c_int,
-                            c_int, c_void_p, c_int, c_int64, c_void_p, c_size_t, c_void_p]),
-    "ft_fp8_gemm_workspace_size": (c_size_t, [c_int, c_int, c_int]),
+                            c_int, c_void_p, c_int, c_int64, c_void_p]),
     "ft_moe_ffn_fp8": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
                                POINTER(SlotLayout), c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
     "ft_moe_ffn_fp8_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
@@ -248,12 +247,8 @@ def fp8_pack(w, N, K, codes, ld_codes, scales, ld_scales, stream) -> None:
     check(lib().ft_fp8_pack(w, N, K, codes, ld_codes, scales, ld_scales, stream))
 
 
-def fp8_gemm_workspace_size(M, N, K) -> int:
-    return int(lib().ft_fp8_gemm_workspace_size(M, N, K))
-
-
-def fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo, ws, ws_bytes, stream) -> None:
-    check(lib().ft_fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo, ws, ws_bytes, stream))
+def fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo, stream) -> None:
+    check(lib().ft_fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo, stream))
 
 
 def ffn_fp8_workspace_size(T, H, I, E, k) -> int:

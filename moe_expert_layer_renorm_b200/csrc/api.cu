@@ -366,14 +366,9 @@ static bool fp8_gemm_shape_ok(int M, int N, int K) {
   return M >= 0 && N >= 1 && K >= 1 && M <= (1 << 24) && N <= (1 << 24) && K < (1 << 24);
 }
 
-extern "C" size_t ft_fp8_gemm_workspace_size(int M, int N, int K) {
-  if (M <= 0 || !fp8_gemm_shape_ok(M, N, K)) return 0;
-  return fp8_gemm_ws_bytes(M, N, K);
-}
-
 extern "C" int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64_t ld_sa, const uint8_t* b,
                            int64_t ldb, const float* sb, int64_t ld_sb, int M, int N, int K, void* out, int out_type,
-                           int64_t ldo, void* ws, size_t ws_bytes, ft_stream_t stream) {
+                           int64_t ldo, ft_stream_t stream) {
   if (!fp8_gemm_shape_ok(M, N, K) || lda < K || ldb < K || lda % 16 || ldb % 16 || ld_sa < fp8_blocks(K) ||
       ld_sb < fp8_blocks(K) || ldo < N || (out_type != FT_F32 && out_type != FT_BF16))
     return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: need N, K >= 1 (M, N, K up to 2^24), code pitches that hold a row and "
@@ -381,12 +376,10 @@ extern "C" int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64
   if (M == 0) return FT_OK;
   if (!a || !sa || !b || !sb || !out) return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: null pointer");
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(sa, 4) || !aligned(sb, 4) ||
-      !aligned(out, out_type == FT_F32 ? 4 : 2) || !aligned(ws, 256))
-    return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: misaligned pointer (codes 16-byte, ws 256-byte)");
-  const size_t need = fp8_gemm_ws_bytes(M, N, K);
-  if (need > 0 && (!ws || ws_bytes < need)) return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: workspace too small");
+      !aligned(out, out_type == FT_F32 ? 4 : 2))
+    return fail(FT_ERR_INVALID_ARG, "ft_fp8_gemm: misaligned pointer (codes must be 16-byte aligned)");
   const char* why = "ft_fp8_gemm";
-  const cudaError_t e = launch_fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo, ws,
+  const cudaError_t e = launch_fp8_gemm(a, lda, sa, ld_sa, b, ldb, sb, ld_sb, M, N, K, out, out_type, ldo,
                                         S(stream), &why);
   return e == cudaSuccess ? FT_OK : cuda_fail(e, why);
 }

@@ -46,9 +46,12 @@ struct Fp8Params {
   long long ldo;
   int out_tma;                // tile kernel: `out` has a tensor map
   float* hs;                  // gate/up: scales of h [rows, ceil(N/128)]
-  float* partials;            // stream kernel: two tiles for each CTA
-  int* counters;              // stream kernel: arrivals at each cut tile, zero between launches
-  int min_blocks;             // stream kernel: the fewest K blocks a CTA takes
+  // stream kernel
+  const int32_t* offsets;     // grouped: group offsets [E + 1] and slots [E]; null: dense
+  const int32_t* slot_table;
+  int E, num_slots;
+  int split;                  // CTAs (one cluster) that share a tile's K blocks
+  int early;                  // weights and groups are older than the kernel before this one
 };
 
 struct Fp8Unit {
@@ -100,10 +103,6 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)
 // skewed tokens took 259 us instead of 176.
 __device__ __forceinline__ float fp8_silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
-__device__ __forceinline__ void store_as(void* out, int type, size_t i, float v) {
-  if (type == FT_F32) static_cast<float*>(out)[i] = v;
-  else static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
-}
 // |v| for a maximum that leaves NaN out, as ordered bits.
 __device__ __forceinline__ uint32_t abs_bits(float v) {
   const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
@@ -112,20 +111,38 @@ __device__ __forceinline__ uint32_t abs_bits(float v) {
 
 // ---------------------------------------------------------- few rows ---
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The cluster address of `p`'s place in the shared memory of CTA `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 template <int NMAT, int BN>
 struct Fp8StreamCfg {
   static constexpr int kStageBytes = NMAT * kFp8WBytes + BN * 128;
-  static constexpr int kStages = 200 * 1024 / kStageBytes < 12 ? 200 * 1024 / kStageBytes : 12;
+  // partial sums from the other CTAs of the cluster; none where they would take more than 32 KB
+  static constexpr int kXBytes = NMAT * BN * 512 <= 32768 ? NMAT * BN * 512 : 0;
+  static constexpr int kStages = (208 * 1024 - kXBytes) / kStageBytes;
   static constexpr int kDB = 4;                        // accumulator buffers
   static constexpr int kTmemCols = kDB * NMAT * BN;    // a power of two, 64 .. 512
-  static constexpr int kBars = 2 * kStages + 2 * kDB + 2;
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kBars * 8 + 4 * BN * 4 + 32;
-  static constexpr int kTileFloats = NMAT * BN * 128;
+  static constexpr int kBars = 2 * kStages + 2 * kDB + 4;
+  static constexpr int kFixedBytes = 1024 + kStages * kStageBytes + kXBytes + kBars * 8 + 4 * BN * 4 + 64;
+  static constexpr int smem_bytes(int E) { return kFixedBytes + 12 * (E + 1); }   // and the groups' table
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
-  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+  static_assert(smem_bytes(1024) <= 227 * 1024, "shared memory");
 };
 
 constexpr int kFp8StreamThreads = 192;   // TMA warp, MMA warp, four epilogue warps
+
 // One lane of a converged warp.  The MMA warps run their loops as a whole warp
 // with warp-uniform values and issue inside this branch: descriptors and
 // addresses then stay in uniform registers.  (Four MMAs of N = 32, their two
@@ -146,7 +163,8 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-constexpr int kTagEpi = 9, kTagOut = 10;  // barrier kinds of a wait timeout: the epilogue warps' own, the output staging's
+// barrier kinds of a wait timeout: the epilogue warps' own, the output staging's, the cluster's exchange
+constexpr int kTagEpi = 9, kTagOut = 10, kTagX = 11;
 
 // A barrier of the epilogue warps: an mbarrier, so that a warp that has given
 // up leaves no other waiting without a limit.
@@ -163,6 +181,123 @@ struct EpiSync {
   }
 };
 
+// The groups as tiles of BN rows, in shared memory: first[e] is expert e's
+// first tile, first[E] their number.
+struct Fp8Groups {
+  int *first, *rb, *slot;
+};
+__device__ void fp8_group_table(const Fp8Params& p, int bn, const Fp8Groups& g, int* warp_sums) {
+  const int per = (p.E + kFp8StreamThreads - 1) / kFp8StreamThreads, e0 = threadIdx.x * per;
+  int sum = 0;
+  for (int e = e0; e < min(p.E, e0 + per); ++e) {
+    const int rb = __ldg(p.offsets + e);
+    int n = __ldg(p.offsets + e + 1) - rb;
+    const int slot = __ldg(p.slot_table + e);
+    if (n > 0 && (slot < 0 || slot >= p.num_slots)) {
+      if (blockIdx.x == 0) set_device_status(slot < 0 ? FT_DEV_NOT_RESIDENT : FT_DEV_BAD_INDEX);
+      n = 0;
+    }
+    g.rb[e] = rb;
+    g.slot[e] = slot;
+    g.first[e] = sum;                    // within this thread's experts, for now
+    sum += n > 0 ? (n + bn - 1) / bn : 0;
+  }
+  const int base = block_exclusive_scan(sum, warp_sums);
+  for (int e = e0; e < min(p.E, e0 + per); ++e) g.first[e] += base;
+  if (threadIdx.x == kFp8StreamThreads - 1) g.first[p.E] = base + sum;
+  __syncthreads();
+}
+
+// The walk of one CTA over its K blocks: tiles cid, cid + ncl, ..., of each the blocks [k0, k1).
+struct Fp8Walk {
+  const Fp8Params& p;
+  const Fp8Groups& g;
+  int bn, units, ncl, k0, k1;
+  int u, kb;
+  Fp8Unit d;
+  __device__ Fp8Walk(const Fp8Params& p_, const Fp8Groups& g_, int bn_, int units_, int cid, int ncl_, int k0_, int k1_)
+      : p(p_), g(g_), bn(bn_), units(units_), ncl(ncl_), k0(k0_), k1(k1_), u(cid), kb(k0_) { find(); }
+  __device__ __forceinline__ bool more() const { return u < units; }
+  __device__ __forceinline__ void find() {
+    if (u >= units) return;
+    const int tile = p.offsets ? u / p.feat_tiles : u % p.row_tiles;
+    d.ft = p.offsets ? u - tile * p.feat_tiles : u / p.row_tiles;
+    if (!p.offsets) {
+      d.slot = 0;
+      d.rb = tile * bn;
+      d.nr = min(bn, p.rows - d.rb);
+      return;
+    }
+    int lo = 0, hi = p.E;                // the last expert whose first tile is <= tile
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (g.first[mid] <= tile) lo = mid; else hi = mid;
+    }
+    const int t = tile - g.first[lo];
+    d.slot = g.slot[lo];
+    d.rb = g.rb[lo] + t * bn;
+    d.nr = min(bn, __ldg(p.offsets + lo + 1) - d.rb);
+  }
+  __device__ __forceinline__ void next_tile() { u += ncl; kb = k0; find(); }
+  __device__ __forceinline__ void next() { if (++kb == k1) next_tile(); }
+};
+
+// Abort::wait for what other CTAs of the cluster wrote.
+__device__ __forceinline__ bool cluster_wait(const Abort& ab, uint64_t* bar, uint32_t parity, long long unit) {
+  if (!ab.wait(bar, parity, kTagX, 0, unit)) return false;
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  return true;
+}
+
+// The partial sums of a tile of nr rows (n < nr of acc[m][n]; this thread's
+// weight row) to the CTAs that finish them, and back the sums of this CTA's
+// columns: acc[m][j] becomes column rank * (BN / S) + j.
+template <int NMAT, int BN, int S>
+__device__ __forceinline__ bool fp8_exchange(float (&acc)[NMAT][BN], float* xbuf, uint64_t* x_full, uint64_t* x_free,
+                                             uint32_t phase, int rank, int nr, int row, int lane, const Abort& ab,
+                                             long long unit) {
+  constexpr int C = BN / S;   // columns a CTA
+  if (!__all_sync(0xFFFFFFFFu, cluster_wait(ab, x_free, phase ^ 1, unit))) return false;   // the last tile's are read
+#pragma unroll
+  for (int q = 0; q < S; ++q) {
+    if (q * C >= nr) break;
+    const uint32_t dst = cluster_addr(xbuf, q) + rank * (NMAT * C * 512) + row * 4;
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+      for (int j = 0; j < C; ++j)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst + (m * C + j) * 512), "f"(acc[m][q * C + j]) : "memory");
+  }
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+  __syncwarp();
+  if (lane < S)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(x_full, lane)) : "memory");
+  if (!__all_sync(0xFFFFFFFFu, cluster_wait(ab, x_full, phase, unit))) return false;
+  if (rank * C < nr) {
+#pragma unroll
+    for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int q = 0; q < S; ++q) sum += xbuf[((q * NMAT + m) * C + j) * 128 + row];
+        acc[m][j] = sum;
+      }
+  }
+  __syncwarp();
+  if (lane < S)
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr(x_free, lane)) : "memory");
+  return true;
+}
+
+// A tile is 128 weight rows x BN token rows.  The K blocks of one tile are
+// shared by the `split` CTAs of a cluster, each of which streams its share
+// of the weights (a full ring of them in flight a SM); the partial sums go
+// through distributed shared memory: each CTA adds up, in the order of the
+// CTAs (the same bits every time), and finishes BN / split of the columns.
+// A tile's weights stand in memory longer than its token rows (`early`: the
+// kernel before this one makes those rows): the first ring of weights is
+// requested before that kernel has ended.
 template <int NMAT, int BN>
 __global__ void __launch_bounds__(kFp8StreamThreads, 1)
 fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
@@ -170,24 +305,35 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   using Cfg = Fp8StreamCfg<NMAT, BN>;
   constexpr int NST = Cfg::kStages, DB = Cfg::kDB;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ int warp_sums[32];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NST * Cfg::kStageBytes);
+  float* xbuf = reinterpret_cast<float*>(smem + NST * Cfg::kStageBytes);   // [source][matrix][BN / split][128]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + NST * Cfg::kStageBytes + Cfg::kXBytes);
   uint64_t* empty = full + NST;
   uint64_t* d_full = empty + NST;
   uint64_t* d_empty = d_full + DB;
   uint64_t* drain_bar = d_empty + DB;
   uint64_t* epi_bar = drain_bar + 1;
-  uint32_t* tmax = reinterpret_cast<uint32_t*>(epi_bar + 1);   // [4][BN]: each epilogue warp's maxima of h
+  uint64_t* x_full = epi_bar + 1;       // the cluster's partial sums of this CTA's columns are here
+  uint64_t* x_free = x_full + 1;        // the cluster has read this CTA's partial sums
+  uint32_t* tmax = reinterpret_cast<uint32_t*>(x_free + 1);   // [4][BN]: each epilogue warp's maxima of h
   uint32_t* tmem_slot = tmax + 4 * BN;
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
-  int* last_flag = abort_flag + 1;
+  Fp8Groups groups;
+  groups.first = abort_flag + 1;
+  groups.rb = groups.first + p.E + 1;
+  groups.slot = groups.rb + p.E + 1;
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // warp-uniform
+  const int S = p.split;
+  const int rank = S > 1 ? cluster_rank() : 0;
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 4); }
     mbar_init(drain_bar, 1);
     mbar_init(epi_bar, 4);
+    mbar_init(x_full, 4 * S);
+    mbar_init(x_free, 4 * S);
     *abort_flag = 0;
     fence_mbarrier_init();
     prefetch_tmap(&tm_w0);
@@ -196,35 +342,41 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   }
   if (warp == 1) { tmem_alloc(tmem_slot, Cfg::kTmemCols); tmem_relinquish(); }
   tc_fence_before();
-  __syncthreads();
+  if (!p.early) pdl_wait();
+  if (p.offsets) fp8_group_table(p, BN, groups, warp_sums);
+  else __syncthreads();
+  if (S > 1) cluster_sync();   // the other CTAs' barriers are in place
   tc_fence_after();
-  pdl_wait();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const Abort ab{abort_flag};
-
-  // this CTA's range of K blocks, all tiles' blocks in one line
-  const int nk = p.nk;
-  const long long total = (long long)(p.units ? *p.num_units : p.row_tiles * p.feat_tiles) * nk;
-  const long long per = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_blocks);
-  const long long g0 = min(total, per * blockIdx.x), g1 = min(total, g0 + per);
+  const int nk = p.nk, per = (nk + S - 1) / S;
+  const int units = p.offsets ? groups.first[p.E] * p.feat_tiles : p.row_tiles * p.feat_tiles;
+  Fp8Walk w(p, groups, BN, units, blockIdx.x / S, gridDim.x / S, rank * per, min(nk, (rank + 1) * per));
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer ---
     if (lane == 0) {
       uint32_t i = 0;
-      bool ok = true;
-      int u = int(g0 / nk), kb = int(g0 - (long long)u * nk);
-      for (long long g = g0; g < g1 && ok; ++u, kb = 0) {
-        const Fp8Unit d = fp8_unit(p, u, BN);
-        for (; kb < nk && g < g1; ++kb, ++g, ++i) {
-          const int s = i % NST;
-          if (!(ok = ab.wait(&empty[s], ((i / NST) & 1) ^ 1, kTagWEmpty, i, u))) break;
-          uint8_t* dst = smem + s * Cfg::kStageBytes;
-          mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
-          tma_load_3d(dst, &tm_w0, &full[s], kb * 128, d.ft * 128, d.slot);
-          if (NMAT > 1) tma_load_3d(dst + kFp8WBytes, &tm_w1, &full[s], kb * 128, d.ft * 128, d.slot);
-          tma_load_2d(dst + NMAT * kFp8WBytes, &tm_rows, &full[s], kb * 128, d.rb);
-        }
+      auto weights = [&](const Fp8Walk& at, int s) {
+        uint8_t* dst = smem + s * Cfg::kStageBytes;
+        mbar_arrive_expect_tx(&full[s], Cfg::kStageBytes);
+        tma_load_3d(dst, &tm_w0, &full[s], at.kb * 128, at.d.ft * 128, at.d.slot);
+        if (NMAT > 1) tma_load_3d(dst + kFp8WBytes, &tm_w1, &full[s], at.kb * 128, at.d.ft * 128, at.d.slot);
+      };
+      auto rows = [&](const Fp8Walk& at, int s) {
+        tma_load_2d(smem + s * Cfg::kStageBytes + NMAT * kFp8WBytes, &tm_rows, &full[s], at.kb * 128, at.d.rb);
+      };
+      if (p.early) {
+        Fp8Walk t = w;
+        for (; i < NST && w.more(); ++i, w.next()) weights(w, i);
+        pdl_wait();
+        for (uint32_t j = 0; j < i; ++j, t.next()) rows(t, j);
+      }
+      for (; w.more(); ++i, w.next()) {
+        const int s = i % NST;
+        if (!ab.wait(&empty[s], ((i / NST) & 1) ^ 1, kTagWEmpty, i, w.u)) break;
+        weights(w, s);
+        rows(w, s);
       }
       for (uint32_t j = (i > NST ? i - NST : 0); j < i; ++j) {   // drain: every copy has landed
         const uint64_t t0 = globaltimer_ns();
@@ -236,32 +388,28 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
     uint32_t i = 0;
     int s = 0, b = 0;
     bool ok = true;
-    int u = int(g0 / nk), kb = int(g0 - (long long)u * nk);
-    for (long long g = g0; g < g1 && ok; ++u, kb = 0) {
-      const int n_eff = (fp8_unit(p, u, BN).nr + 15) & ~15;
-      const uint32_t idesc = make_idesc_e4m3(128, n_eff);
-      for (; kb < nk && g < g1; ++kb, ++g, ++i) {
-        ok = ab.wait(&d_empty[b], ((i / DB) & 1) ^ 1, kTagDEmpty, i, u) &&
-             ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, u);
-        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
-        tc_fence_after();
-        if (elect_one()) {
-          uint8_t* src = smem + s * Cfg::kStageBytes;
-          const uint64_t rd = make_sdesc_sw128(smem_u32(src + NMAT * kFp8WBytes));
+    for (; w.more(); w.next(), ++i) {
+      const uint32_t idesc = make_idesc_e4m3(128, (w.d.nr + 15) & ~15);
+      ok = ab.wait(&d_empty[b], ((i / DB) & 1) ^ 1, kTagDEmpty, i, w.u) &&
+           ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, w.u);
+      if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+      tc_fence_after();
+      if (elect_one()) {
+        uint8_t* src = smem + s * Cfg::kStageBytes;
+        const uint64_t rd = make_sdesc_sw128(smem_u32(src + NMAT * kFp8WBytes));
 #pragma unroll
-          for (int m = 0; m < NMAT; ++m) {
-            const uint64_t wd = make_sdesc_sw128(smem_u32(src + m * kFp8WBytes));
+        for (int m = 0; m < NMAT; ++m) {
+          const uint64_t wd = make_sdesc_sw128(smem_u32(src + m * kFp8WBytes));
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mma_ss_f8(tmem + (b * NMAT + m) * BN, wd + 2 * j, rd + 2 * j, idesc, j > 0);
-          }
-          mma_commit(&empty[s]);
-          mma_commit(&d_full[b]);
+          for (int j = 0; j < 4; ++j)
+            mma_ss_f8(tmem + (b * NMAT + m) * BN, wd + 2 * j, rd + 2 * j, idesc, j > 0);
         }
-        __syncwarp();
-        if (++s == NST) s = 0;
-        if (++b == DB) b = 0;
+        mma_commit(&empty[s]);
+        mma_commit(&d_full[b]);
       }
+      __syncwarp();
+      if (++s == NST) s = 0;
+      if (++b == DB) b = 0;
     }
     if (i > 0) {   // drain: every MMA this warp issued has completed
       if (elect_one()) mma_commit(drain_bar);
@@ -271,19 +419,18 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
     }
   } else {
     // ---------------------------------------------------- epilogue ---
+    if (p.early) pdl_wait();
+    pdl_launch_dependents();   // what follows fits beside this kernel only as its CTAs end
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;                 // weight row within the tile = tensor-memory lane
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     constexpr int kGroups = (BN + 31) / 32;
     EpiSync epi{epi_bar, ab, 0};
-    uint32_t i = 0;
+    uint32_t i = 0, x_phase = 0;
     bool ok = true;
-    const int u0 = int(g0 / nk);
-    int u = u0, kb = int(g0 - (long long)u * nk);
-    for (long long g = g0; g < g1; ++u, kb = 0) {
-      const Fp8Unit d = fp8_unit(p, u, BN);
+    for (; w.more() && ok; w.next_tile(), x_phase ^= 1) {
+      const Fp8Unit d = w.d;
       const int n_eff = (d.nr + 15) & ~15;
-      const bool whole = kb == 0 && g + nk <= g1;
       float acc[NMAT][BN];
 #pragma unroll
       for (int m = 0; m < NMAT; ++m)
@@ -292,7 +439,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
       const float* sw[NMAT];
 #pragma unroll
       for (int m = 0; m < NMAT; ++m) sw[m] = fp8_weight_scales(p, m, d.slot, d.ft);
-      for (; kb < nk && g < g1; ++kb, ++g, ++i) {
+      for (int kb = w.k0; kb < w.k1; ++kb, ++i) {
         float sr[kGroups], ws[NMAT];   // lane j of group q holds the scale of token row 32 q + j
 #pragma unroll
         for (int q = 0; q < kGroups; ++q)
@@ -300,7 +447,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
 #pragma unroll
         for (int m = 0; m < NMAT; ++m) ws[m] = __ldg(sw[m] + kb);
         const int b = i % DB;
-        if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[b], (i / DB) & 1, kTagDFull, i, u)))) break;
+        if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[b], (i / DB) & 1, kTagDFull, i, w.u)))) break;
         tc_fence_after();
         const uint32_t dcol = tmem + lane_base + b * NMAT * BN;
 #pragma unroll
@@ -323,63 +470,48 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
         if (lane == 0) mbar_arrive(&d_empty[b]);
       }
       if (!ok) break;
-      if (!whole) {
-        // a cut tile: leave the partial sums, and the last CTA to arrive adds them all up in range order
-        float* mine = p.partials + ((long long)blockIdx.x * 2 + (u != u0)) * Cfg::kTileFloats + row;
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m)
-#pragma unroll
-          for (int n = 0; n < BN; ++n)
-            if (n < d.nr) __stcg(mine + (m * BN + n) * 128, acc[m][n]);
-        const long long first = (long long)u * nk / per, end = ((long long)(u + 1) * nk - 1) / per;
-        __threadfence();
-        if (!(ok = epi.sync(lane))) break;
-        if (threadIdx.x == 64) *last_flag = atomicAdd(p.counters + u, 1) == int(end - first);
-        if (!(ok = epi.sync(lane))) break;
-        if (!*last_flag) continue;
-        __threadfence();
-        if (threadIdx.x == 64) p.counters[u] = 0;
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m)
-#pragma unroll
-          for (int n = 0; n < BN; ++n) acc[m][n] = 0.0f;
-        for (long long c = first; c <= end; ++c) {
-          // CTA c's first tile unless its range began in an earlier one
-          const bool second = c * per / nk != u;
-          const float* part = p.partials + (c * 2 + second) * Cfg::kTileFloats + row;
-#pragma unroll
-          for (int m = 0; m < NMAT; ++m)
-#pragma unroll
-            for (int n = 0; n < BN; ++n)
-              if (n < d.nr) acc[m][n] += __ldcg(part + (m * BN + n) * 128);
-        }
+      if (Cfg::kXBytes > 0 && S > 1) {
+        ok = S == 2   ? fp8_exchange<NMAT, BN, 2>(acc, xbuf, x_full, x_free, x_phase, rank, d.nr, row, lane, ab, w.u)
+             : S == 4 ? fp8_exchange<NMAT, BN, 4>(acc, xbuf, x_full, x_free, x_phase, rank, d.nr, row, lane, ab, w.u)
+                      : fp8_exchange<NMAT, BN, 8>(acc, xbuf, x_full, x_free, x_phase, rank, d.nr, row, lane, ab, w.u);
+        if (!ok) break;
       }
+      // this CTA's columns: token rows rb0 + j, j < nc
+      const int c0 = rank * (BN / S), nc = min(d.nr - c0, BN / S);
+      const long long rb0 = d.rb + c0;
       const int feat = d.ft * 128 + row;
       if constexpr (NMAT == 1) {
         if (feat < p.N) {
+          const size_t at = rb0 * p.ldo + feat;
+          if (p.out_type == FT_F32) {
 #pragma unroll
-          for (int n = 0; n < BN; ++n)
-            if (n < d.nr) store_as(p.out, p.out_type, (d.rb + n) * p.ldo + feat, acc[0][n]);
+            for (int j = 0; j < BN; ++j)
+              if (j < nc) static_cast<float*>(p.out)[at + j * p.ldo] = acc[0][j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < BN; ++j)
+              if (j < nc) static_cast<__nv_bfloat16*>(p.out)[at + j * p.ldo] = __float2bfloat16_rn(acc[0][j]);
+          }
         }
       } else {
         // h = silu(gate) up; its scale is the maximum over the tile's 128 features (those past N are zeros)
 #pragma unroll
-        for (int n = 0; n < BN; ++n) {
-          if (n >= d.nr) break;
-          acc[0][n] = fp8_silu_mul(acc[0][n], acc[NMAT - 1][n]);
-          const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, abs_bits(acc[0][n]));
-          if (lane == 0) tmax[quarter * BN + n] = m;
+        for (int j = 0; j < BN; ++j) {
+          if (j >= nc) break;
+          acc[0][j] = fp8_silu_mul(acc[0][j], acc[NMAT - 1][j]);
+          const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, abs_bits(acc[0][j]));
+          if (lane == 0) tmax[quarter * BN + j] = m;
         }
         if (!(ok = epi.sync(lane))) break;
         uint8_t* h = static_cast<uint8_t*>(p.out);
         const int hb = (p.N + kFp8Block - 1) / kFp8Block;
 #pragma unroll
-        for (int n = 0; n < BN; ++n) {
-          if (n >= d.nr) break;
-          const uint32_t m = max(max(tmax[n], tmax[BN + n]), max(tmax[2 * BN + n], tmax[3 * BN + n]));
+        for (int j = 0; j < BN; ++j) {
+          if (j >= nc) break;
+          const uint32_t m = max(max(tmax[j], tmax[BN + j]), max(tmax[2 * BN + j], tmax[3 * BN + j]));
           const Fp8Scale f = fp8_scale_of(__uint_as_float(m));
-          if (feat < p.N) h[(d.rb + n) * p.ldo + feat] = uint8_t(cvt_e4m3x2(acc[0][n] * fp8_factor_of(f), 0.0f));
-          if (row == 0) p.hs[(long long)(d.rb + n) * hb + d.ft] = f.scale;
+          if (feat < p.N) h[(rb0 + j) * p.ldo + feat] = uint8_t(cvt_e4m3x2(acc[0][j] * fp8_factor_of(f), 0.0f));
+          if (row == 0) p.hs[(rb0 + j) * hb + d.ft] = f.scale;
         }
         if (!(ok = epi.sync(lane))) break;   // the maxima are read before the next tile's are written
       }
@@ -387,6 +519,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   }
   tc_fence_before();
   __syncthreads();
+  if (S > 1) cluster_sync();   // no CTA leaves while another may still write to it
   pdl_launch_dependents();
   if (warp == 1) {
     tc_fence_after();
@@ -419,20 +552,6 @@ __device__ __forceinline__ void fma2_to(unsigned long long& acc, uint32_t lo, ui
   acc = fma2(pack2(__uint_as_float(lo), __uint_as_float(hi)), s, acc);
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// The cluster address of `p`'s place in the shared memory of CTA `rank`.
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
 // An arrive on a barrier of the pair.  It says only that this warp's tensor
 // memory loads are done (they are waited for); a release at cluster scope
 // would hold the warp until all its memory traffic is visible to the peer,
@@ -877,11 +996,6 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
 
 // ------------------------------------------------------ prep kernels ---
 
-__global__ void __launch_bounds__(256) fp8_zero_kernel(int* counters, int n) {
-  pdl_enter();
-  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += gridDim.x * blockDim.x) counters[i] = 0;
-}
-
 // One launch: blocks [0, sched.nsched) build the two work lists and clear the
 // counters (prep_schedule of ffn.cu), the others write the token rows in FP8
 // in permuted order, eight lanes a group of 128 values.
@@ -962,19 +1076,10 @@ static bool make_fp8_out_map(void* out, int out_type, long long rows, int N, lon
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Launch with the kernel's dynamic shared memory allowed on the current
-// device, in clusters of `cluster` CTAs.
+// A launch in clusters of `cluster` CTAs, allowed to begin while the kernel before it ends.
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_fp8(void (*kern)(KArgs...), int grid, int threads, int smem, int cluster,
-                              std::atomic<uint64_t>& done, cudaStream_t s, Args&&... args) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !(done.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) done.fetch_or(uint64_t(1) << dev);
-  }
+static cudaError_t launch_fp8_grid(void (*kern)(KArgs...), int grid, int threads, int smem, int cluster, cudaStream_t s,
+                                   Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -990,31 +1095,100 @@ static cudaError_t launch_fp8(void (*kern)(KArgs...), int grid, int threads, int
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
+
+// CTAs that the device can hold at once in clusters of `cluster`, of one kernel
+// at one CTA a SM (a property of the device, kept per kernel and device).
+template <typename K>
+static int fp8_cluster_ctas(K kern, int threads, int smem, int cluster, int num_sms, std::atomic<int>* kept) {
+  if (cluster == 1) return num_sms;
+  int n = kept->load();
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms / cluster * cluster);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess || clusters < 1) clusters = num_sms / cluster;
+    n = std::min(clusters, num_sms / cluster) * cluster;
+    kept->store(n);
+  }
+  return n;
+}
+
+// units: the tiles as far as the host can tell, most: their bound.
+//
+// The K blocks of a tile are shared by the split (1, 2, 4, 8) with the least
+// time on the busiest cluster, counted in K blocks: tiles a cluster takes x
+// blocks a CTA, three more a split tile for its exchange (some 2.5 us against
+// 0.75 us a block of gate/up).
 template <int NMAT, int BN>
-static cudaError_t launch_fp8_stream(const Fp8Params& p, int grid, const CUtensorMap& w0, const CUtensorMap& w1,
-                                     const CUtensorMap& rows, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  return launch_fp8(fp8_stream_kernel<NMAT, BN>, grid, kFp8StreamThreads, Fp8StreamCfg<NMAT, BN>::kSmemBytes, 1, done, s,
-                    p, w0, w1, rows);
+static cudaError_t launch_fp8_stream(Fp8Params p, double units, long long most, int num_sms, const CUtensorMap& w0,
+                                     const CUtensorMap& w1, const CUtensorMap& rows, cudaStream_t s) {
+  using Cfg = Fp8StreamCfg<NMAT, BN>;
+  static std::atomic<int> allowed[64], ctas[64][4];   // by device
+  auto kern = fp8_stream_kernel<NMAT, BN>;
+  constexpr int kMost = Cfg::smem_bytes(1024);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  dev &= 63;
+  if (!allowed[dev].load()) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e != cudaSuccess) return e;
+    allowed[dev].store(1);
+  }
+  int cap = num_sms;
+  double best = ceil(units / num_sms) * p.nk;
+  p.split = 1;
+  for (int i = 1; Cfg::kXBytes > 0 && i < 4 && (1 << i) <= p.nk; ++i) {
+    const int S = 1 << i, per = (p.nk + S - 1) / S;
+    if ((S - 1) * per >= p.nk) continue;   // a CTA without a block
+    const int n = fp8_cluster_ctas(kern, kFp8StreamThreads, kMost, S, num_sms, &ctas[dev][i]);
+    const double cost = ceil(units / (n / S)) * (per + 3);
+    if (cost < best - 1e-9) { best = cost; p.split = S; cap = n; }
+  }
+  const int grid = int(std::min<long long>(most * p.split, cap));
+  return launch_fp8_grid(kern, grid, kFp8StreamThreads, Cfg::smem_bytes(p.E), p.split, s, p, w0, w1, rows);
+}
+static int fp8_tile_grid(long long units, bool pair, int num_sms) {
+  return pair ? 2 * int(std::min<long long>(units, num_sms / 2)) : int(std::min<long long>(units, num_sms));
 }
 template <int NMAT, bool PAIR>
-static cudaError_t launch_fp8_tile(const Fp8Params& p, int grid, const CUtensorMap& w0, const CUtensorMap& w1,
-                                   const CUtensorMap& rows, const CUtensorMap& out, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  return launch_fp8(fp8_tile_kernel<NMAT, PAIR>, grid, kFp8TileThreads, Fp8TileCfg<NMAT, PAIR>::kSmemBytes, PAIR ? 2 : 1, done,
-                    s, p, w0, w1, rows, out);
+static cudaError_t launch_fp8_tile(const Fp8Params& p, long long units, int num_sms, const CUtensorMap& w0,
+                                   const CUtensorMap& w1, const CUtensorMap& rows, const CUtensorMap& out, cudaStream_t s) {
+  static std::atomic<uint64_t> done[64];
+  auto kern = fp8_tile_kernel<NMAT, PAIR>;
+  constexpr int kSmem = Fp8TileCfg<NMAT, PAIR>::kSmemBytes;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (!done[dev & 63].load()) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    done[dev & 63].store(1);
+  }
+  return launch_fp8_grid(kern, fp8_tile_grid(units, PAIR, num_sms), kFp8TileThreads, kSmem, PAIR ? 2 : 1, s, p, w0, w1,
+                         rows, out);
 }
+// units: the tiles as far as the host can tell, most: their bound.
 template <int NMAT>
-static cudaError_t launch_fp8_any(int bn, Fp8Params p, long long out_rows, int grid, const CUtensorMap& w0,
-                                  const CUtensorMap& w1, const CUtensorMap& rows, cudaStream_t s) {
+static cudaError_t launch_fp8_any(int bn, Fp8Params p, long long out_rows, double units, long long most,
+                                  const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& rows, cudaStream_t s) {
+  const int num_sms = device_sm_count();
   CUtensorMap out = rows;
   if (bn >= 128 && NMAT == 1) p.out_tma = make_fp8_out_map(p.out, p.out_type, out_rows, p.N, p.ldo, &out);
   switch (bn) {
-    case 16: return launch_fp8_stream<NMAT, 16>(p, grid, w0, w1, rows, s);
-    case 32: return launch_fp8_stream<NMAT, 32>(p, grid, w0, w1, rows, s);
-    case 64: return launch_fp8_stream<NMAT, 64>(p, grid, w0, w1, rows, s);
-    case 128: return launch_fp8_tile<NMAT, false>(p, grid, w0, w1, rows, out, s);
-    default: return launch_fp8_tile<NMAT, true>(p, grid, w0, w1, rows, out, s);
+    case 16: return launch_fp8_stream<NMAT, 16>(p, units, most, num_sms, w0, w1, rows, s);
+    case 32: return launch_fp8_stream<NMAT, 32>(p, units, most, num_sms, w0, w1, rows, s);
+    case 64: return launch_fp8_stream<NMAT, 64>(p, units, most, num_sms, w0, w1, rows, s);
+    case 128: return launch_fp8_tile<NMAT, false>(p, most, num_sms, w0, w1, rows, out, s);
+    default: return launch_fp8_tile<NMAT, true>(p, most, num_sms, w0, w1, rows, out, s);
   }
 }
 
@@ -1041,43 +1215,23 @@ static int fp8_weight_box(int bn, int nmat) {
   return bn < 128 ? 128 : bn == 128 ? (nmat == 2 ? 64 : 256) : (nmat == 2 ? 128 : 64);
 }
 
-static int fp8_tile_grid(long long units, int bn, int num_sms) {
-  return bn == 256 ? 2 * int(std::min<long long>(units, num_sms / 2)) : int(std::min<long long>(units, num_sms));
-}
-
 struct Fp8GemmPlan {
-  int bn, row_tiles, feat_tiles, grid, min_blocks;
-  bool cut;            // a tile may be cut between CTAs
-  size_t off_part, total;
+  int bn, row_tiles, feat_tiles;
 };
-static Fp8GemmPlan plan_fp8_gemm(int M, int N, int K, int num_sms) {
+static Fp8GemmPlan plan_fp8_gemm(int M, int N, int num_sms) {
   Fp8GemmPlan pl{};
-  const int nk = fp8_blocks(K);
   const long long big = ((M + 127LL) / 128) * ((N + 255LL) / 256);
   pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || big * 2 < num_sms ? 64 : M > 512 ? 256 : 128;
   pl.row_tiles = (M + pl.bn - 1) / pl.bn;
   pl.feat_tiles = pl.bn >= 128 ? (N + 255) / 256 : (N + 127) / 128;
-  const long long units = (long long)pl.row_tiles * pl.feat_tiles;
-  pl.min_blocks = 1;
-  if (pl.bn >= 128) {
-    pl.grid = fp8_tile_grid(units, pl.bn, num_sms);
-    return pl;
-  }
-  const long long per = std::max<long long>((units * nk + num_sms - 1) / num_sms, pl.min_blocks);
-  pl.grid = int((units * nk + per - 1) / per);
-  pl.cut = per % nk != 0;
-  if (pl.cut) {
-    pl.off_part = align256(size_t(units) * 4);
-    pl.total = pl.off_part + size_t(pl.grid) * 2 * pl.bn * 128 * 4;
-  }
   return pl;
 }
-static size_t fp8_gemm_ws_bytes(int M, int N, int K) { return plan_fp8_gemm(M, N, K, device_sm_count()).total; }
 
 static cudaError_t launch_fp8_gemm(const uint8_t* a, long long lda, const float* sa, long long ld_sa, const uint8_t* b,
                                    long long ldb, const float* sb, long long ld_sb, int M, int N, int K, void* out,
-                                   int out_type, long long ldo, void* ws, cudaStream_t s, const char** why) {
-  const Fp8GemmPlan pl = plan_fp8_gemm(M, N, K, device_sm_count());
+                                   int out_type, long long ldo, cudaStream_t s, const char** why) {
+  const int num_sms = device_sm_count();
+  const Fp8GemmPlan pl = plan_fp8_gemm(M, N, num_sms);
   CUtensorMap tm_a, tm_b;
   if (!make_fp8_map(a, M, K, lda, 1, 16, fp8_row_box(pl.bn), false, &tm_a) ||
       !make_fp8_map(b, N, K, ldb, 1, ldb * N, fp8_weight_box(pl.bn, 1), true, &tm_b)) {
@@ -1097,50 +1251,37 @@ static cudaError_t launch_fp8_gemm(const uint8_t* a, long long lda, const float*
   p.out = out;
   p.out_type = out_type;
   p.ldo = ldo;
-  p.min_blocks = pl.min_blocks;
-  if (pl.cut) {
-    p.counters = static_cast<int*>(ws);
-    p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + pl.off_part);
-    const int n = pl.row_tiles * pl.feat_tiles;
-    ProfileScope prof(FT_KERNEL_FP8_GEMM, s);
-    const cudaError_t e = launch_pdl(fp8_zero_kernel, dim3(std::min(32, (n + 255) / 256)), dim3(256), 0, s, p.counters, n);
-    if (e != cudaSuccess) return e;
-  }
+  const long long units = (long long)pl.row_tiles * pl.feat_tiles;
   ProfileScope prof(FT_KERNEL_FP8_GEMM, s);
-  return launch_fp8_any<1>(pl.bn, p, M, pl.grid, tm_b, tm_b, tm_a, s);
+  return launch_fp8_any<1>(pl.bn, p, M, double(units), units, tm_b, tm_b, tm_a, s);
 }
 
 struct Fp8FfnPlan {
   int bn, mt1, mt2;                 // token rows a tile takes; feature tiles of gate/up and down
+  double tiles;                     // token tiles, as far as the host can tell
   long long max_units1, max_units2;
-  int grid1, grid2;
-  size_t off_x, off_xs, off_h, off_hs, off_units1, off_units2, off_counts, off_cnt1, off_cnt2, off_part, total;
+  size_t off_x, off_xs, off_h, off_hs, off_units1, off_units2, off_counts, total;
 };
 static Fp8FfnPlan plan_fp8_ffn(int T, int H, int I, int E, int k) {
   Fp8FfnPlan p{};
-  const int num_sms = device_sm_count();
   const long long P = (long long)T * k;
-  const double distinct = E * (1.0 - pow(1.0 - double(k) / E, double(T)));
-  p.bn = fp8_rows_tile(double(P) / std::max(distinct, 1.0));
+  const double distinct = std::max(1.0, E * (1.0 - pow(1.0 - double(k) / E, double(T))));
+  p.bn = fp8_rows_tile(double(P) / distinct);
   p.mt1 = fp8_blocks(I);
   p.mt2 = p.bn >= 128 ? (H + 255) / 256 : fp8_blocks(H);
   const long long tiles = std::min<long long>(E, P) + P / p.bn;
   p.max_units1 = tiles * p.mt1;
   p.max_units2 = tiles * p.mt2;
   const bool stream = p.bn < 128;
-  p.grid1 = stream ? num_sms : fp8_tile_grid(p.max_units1, p.bn, num_sms);
-  p.grid2 = stream ? num_sms : fp8_tile_grid(p.max_units2, p.bn, num_sms);
+  p.tiles = ceil(distinct) * std::max(1.0, ceil(double(P) / distinct / p.bn));
   size_t o = 0;
   p.off_x = o;      o = align256(o + size_t(P) * H);
   p.off_xs = o;     o = align256(o + size_t(P) * fp8_blocks(H) * 4);
   p.off_h = o;      o = align256(o + size_t(P) * I);
   p.off_hs = o;     o = align256(o + size_t(P) * fp8_blocks(I) * 4);
-  p.off_units1 = o; o = align256(o + size_t(p.max_units1) * 16);
-  p.off_units2 = o; o = align256(o + size_t(p.max_units2) * 16);
+  p.off_units1 = o; o = align256(o + (stream ? 0 : size_t(p.max_units1) * 16));
+  p.off_units2 = o; o = align256(o + (stream ? 0 : size_t(p.max_units2) * 16));
   p.off_counts = o; o = align256(o + 16);
-  p.off_cnt1 = o;   o = align256(o + (stream ? size_t(p.max_units1) * 4 : 0));
-  p.off_cnt2 = o;   o = align256(o + (stream ? size_t(p.max_units2) * 4 : 0));
-  p.off_part = o;   o = align256(o + (stream ? size_t(num_sms) * 2 * 2 * p.bn * 128 * 4 : 0));
   p.total = o;
   return p;
 }
@@ -1176,7 +1317,8 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
     sp.slot_table = slot_table;
     sp.E = E;
     sp.num_slots = L.num_slots;
-    sp.nsched = int(std::min<long long>(32, std::max<long long>(1, (pl.max_units1 + pl.max_units2) / 4096)));
+    // the stream kernel finds its tiles itself
+    sp.nsched = stream ? 0 : int(std::min<long long>(32, std::max<long long>(1, (pl.max_units1 + pl.max_units2) / 4096)));
     sp.bn1 = sp.bn2 = pl.bn;
     sp.mt1 = pl.mt1;
     sp.mt2 = pl.mt2;
@@ -1184,10 +1326,6 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
     sp.units1 = units1;
     sp.units2 = units2;
     sp.counts = counts;
-    sp.counters1 = reinterpret_cast<int*>(w + pl.off_cnt1);
-    sp.ncnt1 = stream ? int(pl.max_units1) : 0;
-    sp.counters2 = reinterpret_cast<int*>(w + pl.off_cnt2);
-    sp.ncnt2 = stream ? int(pl.max_units2) : 0;
     sp.perm_src = perm_src;
     sp.P = P;
     sp.k_top = k;
@@ -1209,17 +1347,25 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
   p.slot_bytes = L.slot_bytes;
   p.nk = fp8_blocks(H);
   p.N = I;
-  p.units = units1;
-  p.num_units = counts;
+  if (stream) {
+    // Before this kernel stands the prep kernel, which writes neither weights nor groups, and which began
+    // its own work, and so let this one begin, only when all before it had ended.
+    p.offsets = offsets;
+    p.slot_table = slot_table;
+    p.E = E;
+    p.num_slots = L.num_slots;
+    p.early = 1;
+  } else {
+    p.units = units1;
+    p.num_units = counts;
+  }
+  p.feat_tiles = pl.mt1;
   p.out = w + pl.off_h;
   p.ldo = I;
   p.hs = reinterpret_cast<float*>(w + pl.off_hs);
-  p.partials = reinterpret_cast<float*>(w + pl.off_part);
-  p.counters = reinterpret_cast<int*>(w + pl.off_cnt1);
-  p.min_blocks = 1;
   {
     ProfileScope prof(FT_KERNEL_FP8_GATE_UP, s);
-    e = launch_fp8_any<2>(pl.bn, p, P, pl.grid1, tm[FT_GATE], tm[FT_UP], tm_x, s);
+    e = launch_fp8_any<2>(pl.bn, p, P, pl.tiles * pl.mt1, pl.max_units1, tm[FT_GATE], tm[FT_UP], tm_x, s);
   }
   if (e != cudaSuccess) return e;
   p.sa = reinterpret_cast<const float*>(w + pl.off_hs);
@@ -1228,14 +1374,16 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
   p.ld_sb = L.ld_scale[FT_DOWN] / 4;
   p.nk = fp8_blocks(I);
   p.N = H;
-  p.units = units2;
-  p.num_units = counts + 1;
+  if (!stream) {
+    p.units = units2;
+    p.num_units = counts + 1;
+  }
+  p.feat_tiles = pl.mt2;
   p.out = out;
   p.out_type = out_type;
   p.ldo = H;
-  p.counters = reinterpret_cast<int*>(w + pl.off_cnt2);
   ProfileScope prof(FT_KERNEL_FP8_DOWN, s);
-  return launch_fp8_any<1>(pl.bn, p, P, pl.grid2, tm[FT_DOWN], tm[FT_DOWN], tm_h, s);
+  return launch_fp8_any<1>(pl.bn, p, P, pl.tiles * pl.mt2, pl.max_units2, tm[FT_DOWN], tm[FT_DOWN], tm_h, s);
 }
 
 }  // namespace ftmoe

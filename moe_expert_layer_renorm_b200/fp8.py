@@ -24,22 +24,24 @@ def _blocks(n: int) -> int:
 
 
 def _here(t: torch.Tensor) -> None:
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {t.device}, which is not the current device")
 
 
 def empty_codes(rows: int, K: int, device) -> torch.Tensor:
     """float8 [rows, K] whose rows start on 16 bytes."""
-    return torch.empty((rows, (K + 15) // 16 * 16), dtype=FP8, device=device)[:, :K]
+    codes = torch.empty((rows, (K + 15) // 16 * 16), dtype=FP8, device=device)
+    return codes if K % 16 == 0 else codes[:, :K]
 
 
 def _check_codes(codes: torch.Tensor, scales: torch.Tensor, scale_rows: int, what: str) -> None:
-    if codes.dtype != FP8 or codes.dim() != 2 or (codes.shape[1] > 1 and codes.stride(1) != 1):
+    rows, K = codes.shape if codes.dim() == 2 else (0, 0)
+    if codes.dtype != FP8 or K == 0 or (K > 1 and codes.stride(1) != 1):
         raise ValueError(f"{what}: codes must be float8_e4m3fn [rows, K] with contiguous rows")
-    if scales.dtype != torch.float32 or scales.shape != (scale_rows, _blocks(codes.shape[1])) or \
-            (scales.shape[1] > 1 and scales.stride(1) != 1):
-        raise ValueError(f"{what}: scales must be fp32 [{scale_rows}, {_blocks(codes.shape[1])}]")
-    if codes.device != scales.device or not codes.is_cuda:
+    blocks = (K + 127) // 128
+    if scales.dtype != torch.float32 or scales.shape != (scale_rows, blocks) or (blocks > 1 and scales.stride(1) != 1):
+        raise ValueError(f"{what}: scales must be fp32 [{scale_rows}, {blocks}]")
+    if not codes.is_cuda or codes.get_device() != scales.get_device():
         raise ValueError(f"{what}: codes and scales must be on one CUDA device")
 
 
@@ -55,19 +57,22 @@ def _code_pitch(t: torch.Tensor) -> int:
 def quantize_rows(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
                   stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """x [M, K] (fp32, bf16 or fp16; contiguous rows) -> (codes [M, K], scales [M, ceil(K/128)])."""
-    if x.dtype not in _TYPES or x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
+    kind = _TYPES.get(x.dtype)
+    if kind is None or x.dim() != 2 or not x.is_cuda or (x.shape[1] > 1 and x.stride(1) != 1):
         raise ValueError("quantize_rows: x must be a CUDA matrix of fp32, bf16 or fp16 with contiguous rows")
     _here(x)
     M, K = x.shape
+    given = codes is not None or scales is not None
     if codes is None:
         codes = empty_codes(M, K, x.device)
     if scales is None:
-        scales = torch.empty((M, _blocks(K)), dtype=torch.float32, device=x.device)
-    _check_codes(codes, scales, M, "quantize_rows")
-    if codes.shape != (M, K) or codes.device != x.device:
-        raise ValueError("quantize_rows: codes must have x's shape and device")
-    _lib.fp8_quant_rows(x.data_ptr(), _TYPES[x.dtype], M, K, _pitch(x), codes.data_ptr(), _code_pitch(codes),
-                        scales.data_ptr(), _pitch(scales), _stream(stream))
+        scales = torch.empty((M, (K + 127) // 128), dtype=torch.float32, device=x.device)
+    if given:
+        _check_codes(codes, scales, M, "quantize_rows")
+        if codes.shape != (M, K) or codes.get_device() != x.get_device():
+            raise ValueError("quantize_rows: codes must have x's shape and device")
+    _lib.fp8_quant_rows(x.data_ptr(), kind, M, K, _pitch(x), codes.data_ptr(), _code_pitch(codes), scales.data_ptr(),
+                        _pitch(scales), _stream(stream))
     return codes, scales
 
 
@@ -91,6 +96,7 @@ class Fp8Linear:
         _check_codes(codes, scales, _blocks(codes.shape[0]), "Fp8Linear")
         self.codes, self.scales = codes, scales
         self.N, self.K = codes.shape
+        self._pitches = _code_pitch(codes), _pitch(scales)
 
     @classmethod
     def from_weight(cls, w: torch.Tensor, stream=None) -> "Fp8Linear":
@@ -99,29 +105,22 @@ class Fp8Linear:
     def matmul(self, a: torch.Tensor, a_scales: torch.Tensor, out: Optional[torch.Tensor] = None,
                out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """FP8 rows (codes [M, K], scales [M, ceil(K/128)]) times the weight: [M, N] in out_dtype (bf16 or fp32)."""
-        M = a.shape[0]
+        M, N = a.shape[0], self.N
         _check_codes(a, a_scales, M, "matmul")
-        if a.shape[1] != self.K or a.device != self.codes.device:
+        if a.shape[1] != self.K or a.get_device() != self.codes.get_device():
             raise ValueError("matmul: the rows must have the weight's K and device")
         _here(a)
         if out is None:
             if out_dtype not in (torch.bfloat16, torch.float32):
                 raise ValueError("matmul: out_dtype must be bf16 or fp32")
-            out = torch.empty((M, self.N), dtype=out_dtype, device=a.device)
-        elif out.shape != (M, self.N) or out.dtype not in (torch.bfloat16, torch.float32) or \
-                out.device != a.device or (self.N > 1 and out.stride(1) != 1):
+            out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+        elif out.shape != (M, N) or out.dtype not in (torch.bfloat16, torch.float32) or \
+                out.get_device() != a.get_device() or (N > 1 and out.stride(1) != 1):
             raise ValueError("matmul: out must be bf16 or fp32 [M, N] with contiguous rows, on the rows' device")
-        s = torch.cuda.current_stream() if stream is None else stream
-        need = _lib.fp8_gemm_workspace_size(M, self.N, self.K)
-        ws = None
-        if need:   # of this call alone: calls on other streams and in other graphs have their own
-            ws = torch.empty(need, dtype=torch.uint8, device=a.device)
-            if stream is not None:
-                ws.record_stream(s)
-        _lib.fp8_gemm(a.data_ptr(), _code_pitch(a), a_scales.data_ptr(), _pitch(a_scales), self.codes.data_ptr(),
-                      _code_pitch(self.codes), self.scales.data_ptr(), _pitch(self.scales), M, self.N, self.K,
-                      out.data_ptr(), _TYPES[out.dtype], _pitch(out), 0 if ws is None else ws.data_ptr(), need,
-                      s.cuda_stream)
+        ldb, ld_sb = self._pitches
+        _lib.fp8_gemm(a.data_ptr(), _code_pitch(a), a_scales.data_ptr(), _pitch(a_scales), self.codes.data_ptr(), ldb,
+                      self.scales.data_ptr(), ld_sb, M, N, self.K, out.data_ptr(), _TYPES[out.dtype], _pitch(out),
+                      _stream(stream))
         return out
 
     def forward(self, x: torch.Tensor, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:

@@ -64,23 +64,17 @@ def test_pack_refusals(L):
     assert L.ft_pack_slot(A, 0, ctypes.byref(lay), A, A, None) == INVALID
 
 
-def gemm(L, a=A, lda=128, sa=A, lsa=1, b=A, ldb=128, sb=A, lsb=1, M=4, N=32, K=128, out=A, t=1, ldo=32, ws=A, n=1 << 30):
-    return L.ft_fp8_gemm(a, lda, sa, lsa, b, ldb, sb, lsb, M, N, K, out, t, ldo, ws, n, None)
+def gemm(L, a=A, lda=128, sa=A, lsa=1, b=A, ldb=128, sb=A, lsb=1, M=4, N=32, K=128, out=A, t=1, ldo=32):
+    return L.ft_fp8_gemm(a, lda, sa, lsa, b, ldb, sb, lsb, M, N, K, out, t, ldo, None)
 
 
 def test_gemm_refusals(L):
     assert gemm(L, M=0, a=None, sa=None, out=None) == _lib.FT_OK
     for kw in (dict(M=-1), dict(N=0), dict(K=0), dict(lda=112), dict(lda=136), dict(ldb=120), dict(K=129, lda=144, ldb=144),
                dict(ldo=31), dict(t=2), dict(t=7), dict(a=None), dict(sa=None), dict(b=None), dict(sb=None),
-               dict(out=None), dict(a=A + 8), dict(b=A + 4), dict(sa=A + 2), dict(out=A + 1), dict(ws=A + 16),
+               dict(out=None), dict(a=A + 8), dict(b=A + 4), dict(sa=A + 2), dict(out=A + 1),
                dict(K=1 << 24, lda=1 << 24, ldb=1 << 24, lsa=1 << 20, lsb=1 << 20)):
         assert gemm(L, **kw) == INVALID, kw
-    for M, N, K in ((1, 2048, 2048), (64, 5760, 2880), (200, 100, 4096)):
-        need = _lib.fp8_gemm_workspace_size(M, N, K)
-        if need:
-            assert gemm(L, M=M, N=N, K=K, lda=K, ldb=K, lsa=64, lsb=64, ldo=N, n=need - 1) == INVALID
-            assert gemm(L, M=M, N=N, K=K, lda=K, ldb=K, lsa=64, lsb=64, ldo=N, ws=None) == INVALID
-    assert _lib.fp8_gemm_workspace_size(0, 8, 8) == 0
 
 
 def ffn(L, layout, x=A, T=4, H=256, I=512, E=8, k=2, ps=A, off=A, st=A, pool=A, out=A, t=0, ws=A, n=1 << 30):
