@@ -11,6 +11,7 @@
 // row pitch and the addresses allow it, else 1).
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "sm100.cuh"
 
 namespace ftmoe {
@@ -29,11 +30,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// softmax of one row into v (places past E hold 0).  A row whose logits are
-// all -inf has no probabilities: zeros.
+// This lane's logits of one row (places past E hold -inf).
 template <int V, int NV>
-__device__ __forceinline__ void load_softmax(const float* __restrict__ row, int E, int lane, float (&v)[NV * V]) {
-  float m = -INFINITY;
+__device__ __forceinline__ void load_logits(const float* __restrict__ row, int E, int lane, float (&v)[NV * V]) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = V * (lane + 32 * i);
@@ -45,96 +44,210 @@ __device__ __forceinline__ void load_softmax(const float* __restrict__ row, int 
       v[i] = e < E ? __ldg(row + e) : -INFINITY;
     }
   }
+}
+// This lane's places of a row (16-byte pieces for V = 4; 0 past E).
+template <int V, int NV>
+__device__ __forceinline__ void get_row(const float* row, int E, int lane, float (&v)[NV * V]) {
 #pragma unroll
-  for (int i = 0; i < NV * V; ++i) m = fmaxf(m, v[i]);
-  m = warp_max(m);
-  if (m == -INFINITY) m = 0.0f;      // all -inf: exp gives zeros
-  float z = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV * V; ++i) {
-    v[i] = expf(v[i] - m);
-    z += v[i];
+  for (int i = 0; i < NV; ++i) {
+    const int e = V * (lane + 32 * i);
+    if constexpr (V == 4) {
+      const float4 f = e < E ? *reinterpret_cast<const float4*>(row + e) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+    } else {
+      v[i] = e < E ? row[e] : 0.0f;
+    }
   }
-  z = warp_sum(z);
-  const float inv = z == 0.0f ? 0.0f : 1.0f / z;
+}
+template <int V, int NV>
+__device__ __forceinline__ void put_row(float* row, int E, int lane, const float (&v)[NV * V]) {
 #pragma unroll
-  for (int i = 0; i < NV * V; ++i) v[i] *= inv;
+  for (int i = 0; i < NV; ++i) {
+    const int e = V * (lane + 32 * i);
+    if (e >= E) continue;
+    if constexpr (V == 4) *reinterpret_cast<float4*>(row + e) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    else row[e] = v[i];
+  }
 }
 
-// Partial sums of a CTA's tokens: part_p [grid][E], part_c [grid][E], part_n [grid].
+// e^(logit - largest logit) in place of the logits (0 past E), and 1 / their
+// sum.  A row whose logits are all -inf has no probabilities: zeros and 0.
+// The hardware exponential: 2^-22 of a probability near 1, some 2^-20 of one
+// at e^-10, against the 2^-18 that the sums over thousands of tokens keep.
+template <int N>
+__device__ __forceinline__ void row_exps(float (&v)[N]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+  m = warp_max(m);
+  if (m == -INFINITY) m = 0.0f;      // all -inf: exp gives zeros
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __expf(v[i] - m);
+}
+__device__ __forceinline__ float inverse_sum(float z) { return z == 0.0f ? 0.0f : 1.0f / z; }
+
+constexpr int kBalCluster = 8;   // CTAs that add up their sums through distributed shared memory
+
+// Sums over the tokens, in clusters of eight CTAs: a CTA's warps add up their
+// tokens' probabilities in registers, the CTA its warps', and CTA r of a
+// cluster the eight CTAs' sums of its eighth of the experts.  All additions
+// have a fixed order.  One cluster alone (a small batch) finishes counts and
+// loss itself; more of them leave part_p, part_c [clusters][E] and part_n
+// [clusters] to balance_finish_kernel.  A token's logits are requested behind
+// the token before it.
 template <int V, int NV>
-__global__ void __launch_bounds__(kBalThreads)
-balance_partial_kernel(const float* __restrict__ logits, long long ld, const int32_t* __restrict__ ids,
-                       const uint8_t* __restrict__ valid, int T, int E, int k, float* __restrict__ part_p,
-                       int32_t* __restrict__ part_c, int32_t* __restrict__ part_n) {
+__global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(kBalThreads)
+balance_kernel(const float* __restrict__ logits, long long ld, const int32_t* __restrict__ ids,
+               const uint8_t* __restrict__ valid, int T, int E, int k, float coef, float* __restrict__ part_p,
+               int32_t* __restrict__ part_c, int32_t* __restrict__ part_n, int32_t* __restrict__ counts,
+               int32_t* __restrict__ n_valid, float* __restrict__ loss) {
   pdl_enter();
   extern __shared__ float bal_smem[];
-  float* sums = bal_smem;                                          // [kBalWarps][E]
+  float* sums = bal_smem;                                          // [kBalWarps][E], then [0] the CTA's
   int* cnt = reinterpret_cast<int*>(bal_smem + kBalWarps * E);     // [E], then the valid tokens
+  float* terms = reinterpret_cast<float*>(cnt + E + 1);            // [kBalWarps]
+  float* cta_term = terms + kBalWarps;                             // [1]
   for (int e = threadIdx.x; e <= E; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int step = gridDim.x * kBalWarps;
   float acc[NV * V] = {};
   int n = 0;
-  for (int t = blockIdx.x * kBalWarps + warp; t < T; t += gridDim.x * kBalWarps) {
-    if (valid && !__ldg(valid + t)) continue;
+  int t = blockIdx.x * kBalWarps + warp;
+  float next[NV * V];
+  bool live = t < T && (!valid || __ldg(valid + t));
+  if (live) load_logits<V, NV>(logits + t * ld, E, lane, next);
+  for (; t < T; t += step) {
+    const bool now = live;
+    float p[NV * V];
+#pragma unroll
+    for (int i = 0; i < NV * V; ++i) p[i] = next[i];
+    const int id = now && lane < k ? __ldg(ids + size_t(t) * k + lane) : 0;
+    live = t + step < T && (!valid || __ldg(valid + t + step));
+    if (live) load_logits<V, NV>(logits + (t + step) * ld, E, lane, next);
+    if (!now) continue;
     ++n;
+    row_exps(p);
+    float z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV * V; ++i) z += p[i];
+    const float inv = inverse_sum(warp_sum(z));
+#pragma unroll
+    for (int i = 0; i < NV * V; ++i) acc[i] = fmaf(p[i], inv, acc[i]);
     if (lane < k) {
-      const int e = __ldg(ids + size_t(t) * k + lane);
-      if (e >= 0 && e < E) atomicAdd(cnt + e, 1);
+      if (id >= 0 && id < E) atomicAdd(cnt + id, 1);
       else set_device_status(FT_DEV_BAD_INDEX);
     }
-    float p[NV * V];
-    load_softmax<V, NV>(logits + t * ld, E, lane, p);
-#pragma unroll
-    for (int i = 0; i < NV * V; ++i) acc[i] += p[i];
   }
   if (lane == 0) atomicAdd(cnt + E, n);
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const int e = V * (lane + 32 * i) + c;
-      if (e < E) sums[warp * E + e] = acc[i * V + c];
-    }
+  put_row<V, NV>(sums + warp * E, E, lane, acc);
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kBalWarps; ++w) s += sums[w * E + e];
-    part_p[size_t(blockIdx.x) * E + e] = s;
-    part_c[size_t(blockIdx.x) * E + e] = cnt[e];
+    sums[e] = s;
   }
-  if (threadIdx.x == 0) part_n[blockIdx.x] = cnt[E];
-}
-
-// Adds the partials in block order and forms the loss (one CTA).
-__global__ void __launch_bounds__(1024)
-balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
-                      const int32_t* __restrict__ part_n, int blocks, int E, int k, float coef,
-                      int32_t* __restrict__ counts, int32_t* __restrict__ n_valid, float* __restrict__ loss) {
-  pdl_enter();
-  __shared__ float warp_sums[32];
-  int n = 0;
-  for (int b = 0; b < blocks; ++b) n += part_n[b];
-  const int e = threadIdx.x;
+  cluster_sync();
+  const int rank = cluster_rank(), cid = blockIdx.x / kBalCluster;
+  const bool one = gridDim.x == kBalCluster;
+  const int eighth = (E + kBalCluster - 1) / kBalCluster, e0 = rank * eighth, e1 = min(E, e0 + eighth);
   float term = 0.0f;
-  if (e < E) {
+  for (int e = e0 + threadIdx.x; e < e1; e += blockDim.x) {
+    float ps[kBalCluster];
+    int cs[kBalCluster];
+#pragma unroll
+    for (int r = 0; r < kBalCluster; ++r) {
+      ps[r] = ld_cluster_f32(cluster_addr(sums + e, r));
+      cs[r] = ld_cluster_s32(cluster_addr(cnt + e, r));
+    }
     float p = 0.0f;
     int c = 0;
-    for (int b = 0; b < blocks; ++b) {
-      p += part_p[size_t(b) * E + e];
-      c += part_c[size_t(b) * E + e];
+#pragma unroll
+    for (int r = 0; r < kBalCluster; ++r) { p += ps[r]; c += cs[r]; }
+    if (one) {
+      counts[e] = c;
+      term += float(c) * p;
+    } else {
+      part_p[size_t(cid) * E + e] = p;
+      part_c[size_t(cid) * E + e] = c;
     }
-    counts[e] = c;
+  }
+  int total = 0;
+  if (rank == 0 && threadIdx.x == 0)
+    for (int r = 0; r < kBalCluster; ++r) total += ld_cluster_s32(cluster_addr(cnt + E, r));
+  if (!one) {
+    if (rank == 0 && threadIdx.x == 0) part_n[cid] = total;
+    cluster_sync();   // no CTA leaves while another reads its sums
+    return;
+  }
+  term = warp_sum(term);
+  if (lane == 0) terms[warp] = term;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float s = 0.0f;
+    for (int w = 0; w < kBalWarps; ++w) s += terms[w];
+    *cta_term = s;
+  }
+  cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    float s = 0.0f;
+    for (int r = 0; r < kBalCluster; ++r) s += ld_cluster_f32(cluster_addr(cta_term, r));
+    *n_valid = total;
+    *loss = total > 0 ? coef * float(E) / (float(total) * float(total) * float(k)) * s : 0.0f;
+  }
+  cluster_sync();
+}
+
+// Adds the clusters' sums in their order and forms the loss (one CTA of 1024
+// threads: as many threads an expert as fit, each an even share of the clusters).
+__global__ void __launch_bounds__(1024)
+balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restrict__ part_c,
+                      const int32_t* __restrict__ part_n, int clusters, int E, int k, float coef,
+                      int32_t* __restrict__ counts, int32_t* __restrict__ n_valid, float* __restrict__ loss) {
+  pdl_enter();
+  __shared__ float sp[1024], warp_sums[32];
+  __shared__ int sc[1024];
+  const int slices = 1024 / E, slice = threadIdx.x / E, e = threadIdx.x - slice * E;
+  const int share = (clusters + slices - 1) / slices, c0 = slice * share, c1 = min(clusters, c0 + share);
+  int n = 0;
+  if (threadIdx.x < 32) {
+    for (int b = threadIdx.x; b < clusters; b += 32) n += part_n[b];
+    n = __reduce_add_sync(0xFFFFFFFFu, n);
+  }
+  if (slice < slices) {
+    float p = 0.0f;
+    int c = 0;
+    for (int b0 = c0; b0 < c1; b0 += 16) {
+      float ps[16];
+      int cs[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const bool in = b0 + i < c1;
+        ps[i] = in ? part_p[size_t(b0 + i) * E + e] : 0.0f;
+        cs[i] = in ? part_c[size_t(b0 + i) * E + e] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) { p += ps[i]; c += cs[i]; }
+    }
+    sp[threadIdx.x] = p;
+    sc[threadIdx.x] = c;
+  }
+  __syncthreads();
+  float term = 0.0f;
+  if (int(threadIdx.x) < E) {
+    float p = 0.0f;
+    int c = 0;
+    for (int i = 0; i < slices; ++i) { p += sp[i * E + threadIdx.x]; c += sc[i * E + threadIdx.x]; }
+    counts[threadIdx.x] = c;
     term = float(c) * p;
   }
   term = warp_sum(term);
-  if ((e & 31) == 0) warp_sums[e >> 5] = term;
+  if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = term;
   __syncthreads();
-  if (e < 32) {
-    const float sum = warp_sum(warp_sums[e]);
-    if (e == 0) {
+  if (threadIdx.x < 32) {
+    const float sum = warp_sum(warp_sums[threadIdx.x]);
+    if (threadIdx.x == 0) {
       *n_valid = n;
       *loss = n > 0 ? coef * float(E) / (float(n) * float(n) * float(k)) * sum : 0.0f;
     }
@@ -142,10 +255,10 @@ balance_finish_kernel(const float* __restrict__ part_p, const int32_t* __restric
 }
 
 // One warp per token; the row's gradient passes through shared memory, where
-// the selected experts' own terms are added (in the order j = 0 .. k-1, each
-// place by the lane that owns it: repeated ids add up in a fixed order).
+// the selected experts' own terms are added, one lane an expert (repeated ids
+// add up first, in a fixed order).
 template <int V, int NV>
-__global__ void __launch_bounds__(kBalThreads)
+__global__ void __launch_bounds__(kBalThreads, V * NV <= 16 ? 4 : 2)
 route_backward_kernel(const float* __restrict__ logits, long long ld, const int32_t* __restrict__ ids,
                       const float* __restrict__ w, const float* __restrict__ dw, const uint8_t* __restrict__ valid,
                       int T, int E, int k, float coef, const int32_t* __restrict__ counts,
@@ -156,6 +269,12 @@ route_backward_kernel(const float* __restrict__ logits, long long ld, const int3
   float* cf = bal_smem;                                  // [E] counts
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float* srow = bal_smem + E + warp * E;
+  const int step = gridDim.x * kBalWarps;
+  int t = blockIdx.x * kBalWarps + warp;
+  // a token's logits are requested behind the token (or the counts) before it
+  float next[NV * V] = {};
+  bool live = t < T && (!valid || __ldg(valid + t));
+  if (live && counts) load_logits<V, NV>(logits + t * ld, E, lane, next);
   float scale = 0.0f;
   if (counts) {
     for (int e = threadIdx.x; e < E; e += blockDim.x) cf[e] = float(counts[e]);
@@ -163,67 +282,62 @@ route_backward_kernel(const float* __restrict__ logits, long long ld, const int3
     if (n > 0.0f) scale = (dloss ? *dloss : 1.0f) * coef * float(E) / (n * n * float(k));
   }
   __syncthreads();
-  for (int t = blockIdx.x * kBalWarps + warp; t < T; t += gridDim.x * kBalWarps) {
-    float g[NV * V] = {};
-    const bool live = !valid || __ldg(valid + t);
-    if (live && counts) {
-      load_softmax<V, NV>(logits + t * ld, E, lane, g);
-      float mean = 0.0f;
+  for (; t < T; t += step) {
+    float g[NV * V];
+    const bool now = live;
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-          const int e = V * (lane + 32 * i) + c;
-          if (e < E) mean = fmaf(g[i * V + c], cf[e], mean);
-        }
-      mean = warp_sum(mean);
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-          const int e = V * (lane + 32 * i) + c;
-          if (e < E) g[i * V + c] *= scale * (cf[e] - mean);
-        }
+    for (int i = 0; i < NV * V; ++i) g[i] = next[i];
+    float wj = 0.0f, dj = 0.0f;
+    int id = 0;
+    if (now && dw && lane < k) {
+      wj = __ldg(w + size_t(t) * k + lane);
+      dj = __ldg(dw + size_t(t) * k + lane);
+      id = __ldg(ids + size_t(t) * k + lane);
     }
-    if (live && dw) {
-      const float wj = lane < k ? __ldg(w + size_t(t) * k + lane) : 0.0f;
-      const float dj = lane < k ? __ldg(dw + size_t(t) * k + lane) : 0.0f;
-      const int id = lane < k ? __ldg(ids + size_t(t) * k + lane) : 0;
-      const float mine = wj * (dj - warp_sum(wj * dj));
+    live = t + step < T && (!valid || __ldg(valid + t + step));
+    if (live && counts) load_logits<V, NV>(logits + (t + step) * ld, E, lane, next);
+    if (now && counts) {
+      row_exps(g);
+      float z = 0.0f, zc = 0.0f, cv[NV * V];
+      get_row<V, NV>(cf, E, lane, cv);
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-          const int e = V * (lane + 32 * i) + c;
-          if (e < E) srow[e] = g[i * V + c];
-        }
-      for (int j = 0; j < k; ++j) {
-        const int e = __shfl_sync(0xFFFFFFFFu, id, j);
-        const float add = __shfl_sync(0xFFFFFFFFu, mine, j);
-        if (e < 0 || e >= E) {
-          if (lane == 0) set_device_status(FT_DEV_BAD_INDEX);
-        } else if (((e / V) & 31) == lane) {
-          srow[e] += add;
-        }
+      for (int i = 0; i < NV * V; ++i) {
+        z += g[i];
+        zc = fmaf(g[i], cv[i], zc);
       }
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+      for (int off = 16; off > 0; off >>= 1) {   // the two sums side by side
+        z += __shfl_xor_sync(0xFFFFFFFFu, z, off);
+        zc += __shfl_xor_sync(0xFFFFFFFFu, zc, off);
+      }
+      const float inv = inverse_sum(z), mean = zc * inv, f = scale * inv;
 #pragma unroll
-        for (int c = 0; c < V; ++c) {
-          const int e = V * (lane + 32 * i) + c;
-          if (e < E) g[i * V + c] = srow[e];
+      for (int i = 0; i < NV * V; ++i) g[i] *= f * (cv[i] - mean);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV * V; ++i) g[i] = 0.0f;
+    }
+    if (now && dw) {
+      const float mine = wj * (dj - warp_sum(wj * dj));
+      put_row<V, NV>(srow, E, lane, g);
+      // the lowest lane of those with one id adds their terms, in lane order
+      const bool sel = lane < k;
+      if (sel && (id < 0 || id >= E)) set_device_status(FT_DEV_BAD_INDEX);
+      const uint32_t peers = __match_any_sync(0xFFFFFFFFu, sel ? id : -1 - lane);
+      float total = mine;
+      if (__any_sync(0xFFFFFFFFu, __popc(peers) > 1)) {
+        total = 0.0f;
+        for (int j = 0; j < k; ++j) {
+          const float add = __shfl_sync(0xFFFFFFFFu, mine, j);
+          if (peers >> j & 1) total += add;
         }
+      }
+      __syncwarp();
+      if (sel && id >= 0 && id < E && __ffs(peers) - 1 == lane) srow[id] += total;
+      __syncwarp();
+      get_row<V, NV>(srow, E, lane, g);
     }
-    float* out = dlogits + t * ldd;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = V * (lane + 32 * i);
-      if (e >= E) continue;
-      if constexpr (V == 4)
-        *reinterpret_cast<float4*>(out + e) = make_float4(g[4 * i], g[4 * i + 1], g[4 * i + 2], g[4 * i + 3]);
-      else
-        out[e] = g[i];
-    }
+    put_row<V, NV>(dlogits + t * ldd, E, lane, g);
   }
 }
 
@@ -245,34 +359,36 @@ static cudaError_t balance_variant(int E, bool vec, F f) {
   return f(integral_constant<int, 1>(), integral_constant<int, 32>());
 }
 
-static int balance_blocks(int T, int num_sms) {
-  return int(std::min<long long>((T + kBalWarps - 1) / kBalWarps, num_sms));
+// Clusters for T tokens: one, which needs no second launch, up to four tokens a
+// warp (T = 256), else enough for a CTA a SM: more of them cost more in sums
+// than they hide (8192 x 512: F1 us forward, with two a SM F2, with four F4).
+static int balance_clusters(int T, int num_sms) {
+  if (T <= 4 * kBalWarps * kBalCluster) return 1;
+  return std::max(1, std::min((T + kBalWarps * kBalCluster - 1) / (kBalWarps * kBalCluster), num_sms / kBalCluster));
 }
 static size_t balance_ws_bytes(int T, int E, int num_sms) {
-  return size_t(balance_blocks(T, num_sms)) * (2 * size_t(E) + 1) * 4;
+  return size_t(balance_clusters(T, num_sms)) * (2 * size_t(E) + 1) * 4;
 }
 
 static cudaError_t launch_balance(const float* logits, long long ld, const int32_t* ids, const uint8_t* valid, int T,
                                   int E, int k, float coef, int32_t* counts, int32_t* n_valid, float* loss, void* ws,
                                   int num_sms, cudaStream_t s) {
-  const int blocks = balance_blocks(T, num_sms);
+  const int clusters = balance_clusters(T, num_sms);
   float* part_p = static_cast<float*>(ws);
-  int32_t* part_c = reinterpret_cast<int32_t*>(part_p + size_t(blocks) * E);
-  int32_t* part_n = part_c + size_t(blocks) * E;
-  if (T > 0) {
-    const bool vec = E % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
-    const cudaError_t e = balance_variant(E, vec, [&](auto v, auto nv) {
-      ProfileScope prof(FT_KERNEL_BALANCE, s);
-      return launch_pdl(balance_partial_kernel<decltype(v)::value, decltype(nv)::value>, dim3(blocks),
-                        dim3(kBalThreads), ((kBalWarps + 1) * size_t(E) + 1) * 4, s, logits, ld, ids, valid, T, E, k,
-                        part_p, part_c, part_n);
-    });
-    if (e != cudaSuccess) return e;
-  }
+  int32_t* part_c = reinterpret_cast<int32_t*>(part_p + size_t(clusters) * E);
+  int32_t* part_n = part_c + size_t(clusters) * E;
+  const bool vec = E % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
+  const cudaError_t e = balance_variant(E, vec, [&](auto v, auto nv) {
+    ProfileScope prof(FT_KERNEL_BALANCE, s);
+    return launch_pdl(balance_kernel<decltype(v)::value, decltype(nv)::value>, dim3(clusters * kBalCluster),
+                      dim3(kBalThreads), ((kBalWarps + 1) * size_t(E) + kBalWarps + 4) * 4, s, logits, ld, ids, valid, T,
+                      E, k, coef, part_p, part_c, part_n, counts, n_valid, loss);
+  });
+  if (e != cudaSuccess || clusters == 1) return e;
   ProfileScope prof(FT_KERNEL_BALANCE, s);
   return launch_pdl(balance_finish_kernel, dim3(1), dim3(1024), 0, s, static_cast<const float*>(part_p),
-                    static_cast<const int32_t*>(part_c), static_cast<const int32_t*>(part_n), blocks, E, k, coef, counts,
-                    n_valid, loss);
+                    static_cast<const int32_t*>(part_c), static_cast<const int32_t*>(part_n), clusters, E, k, coef,
+                    counts, n_valid, loss);
 }
 
 static cudaError_t launch_route_backward(const float* logits, long long ld, const int32_t* ids, const float* w,

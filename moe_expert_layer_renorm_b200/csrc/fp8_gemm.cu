@@ -25,6 +25,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include "cluster.cuh"
 #include "sm100.cuh"
 
 namespace ftmoe {
@@ -110,21 +111,6 @@ __device__ __forceinline__ uint32_t abs_bits(float v) {
 }
 
 // ---------------------------------------------------------- few rows ---
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-// The cluster address of `p`'s place in the shared memory of CTA `rank`.
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-}
 
 template <int NMAT, int BN>
 struct Fp8StreamCfg {
