@@ -414,6 +414,7 @@ FT_API int ft_fp8_quant_rows(const void* x, int x_type, int M, int K, int64_t ld
  * An fp32 weight [N, K] (device, contiguous) to FP8 in 128 x 128 blocks.
  *   codes   device uint8 [N, K] (out), row pitch ld_codes bytes, a multiple of 16; 16-byte aligned
  *   scales  device fp32 [ceil(N/128), ld_scales] (out; columns past ceil(K/128) zeroed)
+ * N <= 128 * 65535.
  */
 FT_API int ft_fp8_pack(const float* w, int N, int K, uint8_t* codes, int64_t ld_codes, float* scales,
                        int ld_scales, ft_stream_t stream);
@@ -426,7 +427,7 @@ FT_API int ft_fp8_pack(const float* w, int N, int K, uint8_t* codes, int64_t ld_
  *   sa        device fp32 [M, ceil(K/128)], row pitch ld_sa elements
  *   sb        device fp32 [ceil(N/128), ceil(K/128)], row pitch ld_sb elements
  *   out       device [M, N] of type out_type (FT_F32 or FT_BF16), row pitch ldo elements (out)
- * Any M, N, K from 1 up (K < 2^24); no alignment of M, N or K is needed.  M = 0 is a no-op.  No workspace.
+ * Any M, N, K from 1 up (M, N <= 2^24, K < 2^24); no alignment of M, N or K is needed.  M = 0 is a no-op.  No workspace.
  */
 FT_API int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64_t ld_sa, const uint8_t* b,
                        int64_t ldb, const float* sb, int64_t ld_sb, int M, int N, int K, void* out, int out_type,
@@ -443,7 +444,9 @@ FT_API int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64_t l
  * Arguments as for ft_moe_ffn_nvfp4, with an FP8 layout; out_perm is device
  * [T*k, H] of type out_type (FT_F32, or FT_BF16: half the bytes, read by
  * ft_moe_combine_bf16); ws holds ft_moe_ffn_fp8_workspace_size bytes, 256-byte
- * aligned, and needs no zeroing.  A non-empty group whose slot is -1 sets
+ * aligned, needs no zeroing and serves one call at a time (calls that may run
+ * at once, captured graphs among them, each take their own).
+ * T*k <= 2^24 and T*k*ceil(max(H, I)/128) < 2^31.  A non-empty group whose slot is -1 sets
  * FT_DEV_NOT_RESIDENT and its rows are left unwritten, as are rows behind
  * expert_offsets[E]; a slot or a token out of range sets FT_DEV_BAD_INDEX (the
  * rows of that slot are left unwritten, a row of that token reads as zeros).
@@ -475,7 +478,7 @@ FT_API int ft_moe_combine_bf16(const void* out_perm, const int32_t* pair_to_row,
  *   topk_ids  device int32 [T, k] (from ft_moe_route; those of tokens that are not valid are not read)
  *   valid     device uint8 [T], or NULL
  *   counts    device int32 [E] (out), n_valid device int32 [1] (out): Tv, loss device fp32 [1] (out)
- *   ws        device workspace of ft_moe_balance_workspace_size bytes, 16-byte aligned; no zeroing
+ *   ws        device workspace of ft_moe_balance_workspace_size bytes, 16-byte aligned; no zeroing; one call at a time
  * Requires 1 <= k <= min(E, 32), E <= 1024.  An id outside [0, E) sets
  * FT_DEV_BAD_INDEX and is not counted; an id that a token repeats counts each time.
  * A row whose logits are all -inf has no probabilities (p = 0).  Deterministic.

@@ -384,8 +384,14 @@ extern "C" int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64
   return e == cudaSuccess ? FT_OK : cuda_fail(e, why);
 }
 
+// T * k rows of at most 2^31 - 1 blocks of 128 in all
+static bool fp8_ffn_shape_ok(int T, int H, int I, int E, int k) {
+  return ffn_shape_ok(H, I, E, k) && (long long)T * k <= (1 << 24) &&
+         (long long)T * k * fp8_blocks(std::max(H, I)) < (1LL << 31);
+}
+
 extern "C" size_t ft_moe_ffn_fp8_workspace_size(int T, int H, int I, int E, int k) {
-  if (T <= 0 || !ffn_shape_ok(H, I, E, k) || (long long)T * k > (1 << 24)) return 0;
+  if (T <= 0 || !fp8_ffn_shape_ok(T, H, I, E, k)) return 0;
   return plan_fp8_ffn(T, H, I, E, k).total;
 }
 
@@ -393,9 +399,10 @@ extern "C" int ft_moe_ffn_fp8(const void* x, int T, int H, int I, int E, int k, 
                               const int32_t* expert_offsets, const int32_t* slot_table, const void* slot_pool,
                               const ft_nvfp4_slot_layout* layout, void* out_perm, int out_type, void* ws,
                               size_t ws_bytes, ft_stream_t stream) {
-  if (T < 0 || !ffn_shape_ok(H, I, E, k) || (long long)T * k > (1 << 24))
+  if (T < 0 || !fp8_ffn_shape_ok(T, H, I, E, k))
     return fail(FT_ERR_UNSUPPORTED,
-                "ft_moe_ffn_fp8: need H, I >= 256 and multiples of 64, 1 <= k <= E <= 1024, T*k <= 2^24");
+                "ft_moe_ffn_fp8: need H, I >= 256 and multiples of 64, 1 <= k <= E <= 1024, T*k <= 2^24 and "
+                "T*k*ceil(max(H, I)/128) < 2^31");
   if (out_type != FT_F32 && out_type != FT_BF16)
     return fail(FT_ERR_INVALID_ARG, "ft_moe_ffn_fp8: out_type must be f32 or bf16");
   if (T == 0) return FT_OK;

@@ -361,7 +361,8 @@ static cudaError_t balance_variant(int E, bool vec, F f) {
 
 // Clusters for T tokens: one, which needs no second launch, up to four tokens a
 // warp (T = 256), else enough for a CTA a SM: more of them cost more in sums
-// than they hide (8192 x 512: F1 us forward, with two a SM F2, with four F4).
+// than they hide (8192 x 512, loss and gradient: 21.3 us, with two a SM 22.0,
+// with four 25.3).
 static int balance_clusters(int T, int num_sms) {
   if (T <= 4 * kBalWarps * kBalCluster) return 1;
   return std::max(1, std::min((T + kBalWarps * kBalCluster - 1) / (kBalWarps * kBalCluster), num_sms / kBalCluster));

@@ -9,10 +9,9 @@
 // Two orientations:
 //   few rows  (fp8_stream_kernel): the MMA's M side is 128 weight rows, its N
 //     side up to BN token rows; bound by the weight bytes.  The grid's CTAs
-//     share the K blocks of all output tiles evenly: each takes one contiguous
-//     range of (tile, K block) pairs, and the partial sums of a tile that a
-//     range border cuts are added by the last CTA to finish, in range order
-//     (the same bits every time).
+//     form clusters of 1, 2, 4 or 8 that share a tile's K blocks; the partial
+//     sums meet through distributed shared memory and are added in the order
+//     of the cluster's ranks (the same bits every time).
 //   many rows (fp8_tile_kernel): the M side is 128 token rows, the N side 256
 //     weight rows (256 output features; or 128 gate and 128 up rows of the same
 //     features); a row's scales are one number a thread.
@@ -21,6 +20,8 @@
 // reads as zeros.
 //
 // Every pipeline wait is bounded as in ffn.cu.
+#include <type_traits>
+
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -45,7 +46,6 @@ struct Fp8Params {
   void* out;                  // [rows, N], pitch ldo; for gate/up the codes of h
   int out_type;
   long long ldo;
-  int out_tma;                // tile kernel: `out` has a tensor map
   float* hs;                  // gate/up: scales of h [rows, ceil(N/128)]
   // stream kernel
   const int32_t* offsets;     // grouped: group offsets [E + 1] and slots [E]; null: dense
@@ -97,11 +97,14 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)
       : "r"(taddr) : "memory");
 }
 
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld_32x32b_x16(taddr, v); }
+
 // silu(g) u with the hardware exponential and a fast divide: a few fp32 steps
 // (as the exponential overflows the quotient goes to 0, its limit).  One h a
 // thread and column stands between a tile's last block and the next tile's
-// first: with expf and two IEEE divisions here the gate/up kernel of 4096
-// skewed tokens took 259 us instead of 176.
+// first: with expf and an IEEE division here the gate/up kernel of 4096 skewed
+// tokens (2048 x 768, 128 experts, k = 8) takes 197 us instead of 149.
 __device__ __forceinline__ float fp8_silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // |v| for a maximum that leaves NaN out, as ordered bits.
@@ -114,20 +117,25 @@ __device__ __forceinline__ uint32_t abs_bits(float v) {
 
 template <int NMAT, int BN>
 struct Fp8StreamCfg {
+  // Two sets of four epilogue warps take turns at the tiles where registers allow: a down tile of 6 blocks is finished
+  // in some 7000 cycles, longer than its weights take to arrive.
+  static constexpr int kSets = NMAT * BN <= 64 ? 2 : 1;
+  static constexpr int kThreads = 64 + 128 * kSets;             // TMA warp, MMA warp, epilogue warps
   static constexpr int kStageBytes = NMAT * kFp8WBytes + BN * 128;
   // partial sums from the other CTAs of the cluster; none where they would take more than 32 KB
   static constexpr int kXBytes = NMAT * BN * 512 <= 32768 ? NMAT * BN * 512 : 0;
   static constexpr int kStages = (208 * 1024 - kXBytes) / kStageBytes;
-  static constexpr int kDB = 4;                        // accumulator buffers
-  static constexpr int kTmemCols = kDB * NMAT * BN;    // a power of two, 64 .. 512
-  static constexpr int kBars = 2 * kStages + 2 * kDB + 4;
-  static constexpr int kFixedBytes = 1024 + kStages * kStageBytes + kXBytes + kBars * 8 + 4 * BN * 4 + 64;
+  // accumulator buffers, as many as tensor memory holds up to 16: the MMAs, and with them the stream of weights,
+  // run on while the epilogue finishes a tile (4400 cycles) and meets the next one's scales (3500, from HBM)
+  static constexpr int kDB = 512 / (NMAT * BN) < 16 ? 512 / (NMAT * BN) : 16;
+  static constexpr int kTmemCols = kDB * NMAT * BN;    // a power of two, 256 or 512
+  static constexpr int kBars = (2 * kStages + 2 * kDB + 3 + kSets + 1) / 2 * 2;   // even: what follows is 16-byte aligned
+  static constexpr int kFixedBytes = 1024 + kStages * kStageBytes + kXBytes + kBars * 8 + kSets * 8 * BN * 4 + 64;
   static constexpr int smem_bytes(int E) { return kFixedBytes + 12 * (E + 1); }   // and the groups' table
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
   static_assert(smem_bytes(1024) <= 227 * 1024, "shared memory");
 };
 
-constexpr int kFp8StreamThreads = 192;   // TMA warp, MMA warp, four epilogue warps
 
 // One lane of a converged warp.  The MMA warps run their loops as a whole warp
 // with warp-uniform values and issue inside this branch: descriptors and
@@ -167,13 +175,17 @@ struct EpiSync {
   }
 };
 
+__device__ __forceinline__ void fma2_to(unsigned long long& acc, uint32_t lo, uint32_t hi, unsigned long long s) {
+  acc = fma2(pack2(__uint_as_float(lo), __uint_as_float(hi)), s, acc);
+}
+
 // The groups as tiles of BN rows, in shared memory: first[e] is expert e's
 // first tile, first[E] their number.
 struct Fp8Groups {
   int *first, *rb, *slot;
 };
 __device__ void fp8_group_table(const Fp8Params& p, int bn, const Fp8Groups& g, int* warp_sums) {
-  const int per = (p.E + kFp8StreamThreads - 1) / kFp8StreamThreads, e0 = threadIdx.x * per;
+  const int per = (p.E + blockDim.x - 1) / blockDim.x, e0 = threadIdx.x * per;
   int sum = 0;
   for (int e = e0; e < min(p.E, e0 + per); ++e) {
     const int rb = __ldg(p.offsets + e);
@@ -190,7 +202,10 @@ __device__ void fp8_group_table(const Fp8Params& p, int bn, const Fp8Groups& g, 
   }
   const int base = block_exclusive_scan(sum, warp_sums);
   for (int e = e0; e < min(p.E, e0 + per); ++e) g.first[e] += base;
-  if (threadIdx.x == kFp8StreamThreads - 1) g.first[p.E] = base + sum;
+  if (threadIdx.x == blockDim.x - 1) {
+    g.first[p.E] = base + sum;
+    g.rb[p.E] = __ldg(p.offsets + p.E);
+  }
   __syncthreads();
 }
 
@@ -222,7 +237,7 @@ struct Fp8Walk {
     const int t = tile - g.first[lo];
     d.slot = g.slot[lo];
     d.rb = g.rb[lo] + t * bn;
-    d.nr = min(bn, __ldg(p.offsets + lo + 1) - d.rb);
+    d.nr = min(bn, g.rb[lo + 1] - d.rb);
   }
   __device__ __forceinline__ void next_tile() { u += ncl; kb = k0; find(); }
   __device__ __forceinline__ void next() { if (++kb == k1) next_tile(); }
@@ -285,11 +300,11 @@ __device__ __forceinline__ bool fp8_exchange(float (&acc)[NMAT][BN], float* xbuf
 // kernel before this one makes those rows): the first ring of weights is
 // requested before that kernel has ended.
 template <int NMAT, int BN>
-__global__ void __launch_bounds__(kFp8StreamThreads, 1)
+__global__ void __launch_bounds__(Fp8StreamCfg<NMAT, BN>::kThreads, 1)
 fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
                   const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_rows) {
   using Cfg = Fp8StreamCfg<NMAT, BN>;
-  constexpr int NST = Cfg::kStages, DB = Cfg::kDB;
+  constexpr int NST = Cfg::kStages, DB = Cfg::kDB, DBS = DB / Cfg::kSets;   // DBS: accumulator buffers of one set
   extern __shared__ uint8_t smem_raw[];
   __shared__ int warp_sums[32];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -299,11 +314,13 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   uint64_t* d_full = empty + NST;
   uint64_t* d_empty = d_full + DB;
   uint64_t* drain_bar = d_empty + DB;
-  uint64_t* epi_bar = drain_bar + 1;
-  uint64_t* x_full = epi_bar + 1;       // the cluster's partial sums of this CTA's columns are here
+  uint64_t* x_full = drain_bar + 1;     // the cluster's partial sums of this CTA's columns are here
   uint64_t* x_free = x_full + 1;        // the cluster has read this CTA's partial sums
-  uint32_t* tmax = reinterpret_cast<uint32_t*>(x_free + 1);   // [4][BN]: each epilogue warp's maxima of h
-  uint32_t* tmem_slot = tmax + 4 * BN;
+  uint64_t* epi_bar = x_free + 1;       // [set]
+  // of each epilogue warp: a block's row scales [BN], and its maxima of h [BN]
+  float* srow = reinterpret_cast<float*>(full + Cfg::kBars);
+  uint32_t* tmax0 = reinterpret_cast<uint32_t*>(srow + Cfg::kSets * 4 * BN);
+  uint32_t* tmem_slot = tmax0 + Cfg::kSets * 4 * BN;
   int* abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
   Fp8Groups groups;
   groups.first = abort_flag + 1;
@@ -317,7 +334,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
     for (int i = 0; i < NST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < DB; ++i) { mbar_init(&d_full[i], 1); mbar_init(&d_empty[i], 4); }
     mbar_init(drain_bar, 1);
-    mbar_init(epi_bar, 4);
+    for (int i = 0; i < Cfg::kSets; ++i) mbar_init(&epi_bar[i], 4);
     mbar_init(x_full, 4 * S);
     mbar_init(x_free, 4 * S);
     *abort_flag = 0;
@@ -331,12 +348,13 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   if (!p.early) pdl_wait();
   if (p.offsets) fp8_group_table(p, BN, groups, warp_sums);
   else __syncthreads();
-  if (S > 1) cluster_sync();   // the other CTAs' barriers are in place
+  if (S > 1) cluster_arrive();   // this CTA's barriers are in place; the others' are waited for before their first use
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   const Abort ab{abort_flag};
   const int nk = p.nk, per = (nk + S - 1) / S;
   const int units = p.offsets ? groups.first[p.E] * p.feat_tiles : p.row_tiles * p.feat_tiles;
+  bool joined = false;   // whether this thread has waited for the cluster's CTAs
   Fp8Walk w(p, groups, BN, units, blockIdx.x / S, gridDim.x / S, rank * per, min(nk, (rank + 1) * per));
 
   if (warp == 0) {
@@ -372,11 +390,13 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
   } else if (warp == 1) {
     // ------------------------------------------------- MMA issuer ---
     uint32_t i = 0;
-    int s = 0, b = 0;
+    uint32_t c = 0, other = 0;   // blocks given to the set at hand and to the other one
+    int s = 0, set = 0;
     bool ok = true;
-    for (; w.more(); w.next(), ++i) {
+    while (w.more()) {
+      const uint32_t b = set * DBS + c % DBS;
       const uint32_t idesc = make_idesc_e4m3(128, (w.d.nr + 15) & ~15);
-      ok = ab.wait(&d_empty[b], ((i / DB) & 1) ^ 1, kTagDEmpty, i, w.u) &&
+      ok = ab.wait(&d_empty[b], ((c / DBS) & 1) ^ 1, kTagDEmpty, i, w.u) &&
            ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, w.u);
       if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
       tc_fence_after();
@@ -395,7 +415,16 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
       }
       __syncwarp();
       if (++s == NST) s = 0;
-      if (++b == DB) b = 0;
+      ++i;
+      ++c;
+      const int u = w.u;
+      w.next();
+      if (Cfg::kSets == 2 && S == 1 && w.u != u) {   // the next tile is the other set's
+        const uint32_t t = c;
+        c = other;
+        other = t;
+        set ^= 1;
+      }
     }
     if (i > 0) {   // drain: every MMA this warp issued has completed
       if (elect_one()) mma_commit(drain_bar);
@@ -407,34 +436,69 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
     // ---------------------------------------------------- epilogue ---
     if (p.early) pdl_wait();
     pdl_launch_dependents();   // what follows fits beside this kernel only as its CTAs end
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, set = (warp - 2) >> 2;
+    // the sets take every kSets-th tile of this CTA; a split tile's exchange is one set's alone
+    const int turns = S > 1 ? 1 : Cfg::kSets;
     const int row = quarter * 32 + lane;                 // weight row within the tile = tensor-memory lane
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     constexpr int kGroups = (BN + 31) / 32;
-    EpiSync epi{epi_bar, ab, 0};
-    uint32_t i = 0, x_phase = 0;
+    EpiSync epi{epi_bar + set, ab, 0};
+    float* sw = srow + (warp - 2) * BN;
+    uint32_t* tmax = tmax0 + set * 4 * BN;
+    uint32_t i = 0, x_phase = 0;                         // i: blocks of this set so far
+    if (set > 0 && turns == 1) w.u = w.units;            // nothing for this set
     bool ok = true;
-    for (; w.more() && ok; w.next_tile(), x_phase ^= 1) {
-      const Fp8Unit d = w.d;
+    // Scales: lane j holds the weights' of block kb0 + j, 32 blocks at a time, and those of token row 32 q + j for
+    // the next two blocks.  A tile's first ones are requested before the tile before it is finished.
+    Fp8Unit d = {};
+    const float* wp[NMAT];
+    float wl[NMAT], sr[kGroups], sr1[kGroups], sr2[kGroups];
+    auto row_scales = [&](int kb, float (&v)[kGroups]) {
+#pragma unroll
+      for (int q = 0; q < kGroups; ++q)
+        v[q] = q * 32 + lane < d.nr && kb < w.k1 ? __ldg(p.sa + (d.rb + q * 32 + lane) * p.ld_sa + kb) : 0.0f;
+    };
+    auto weight_scales = [&](int kb) {
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) wl[m] = kb + lane < w.k1 ? __ldg(wp[m] + kb + lane) : 0.0f;
+    };
+    auto begin_tile = [&]() {
+      d = w.d;
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m) wp[m] = fp8_weight_scales(p, m, d.slot, d.ft);
+      weight_scales(w.k0);
+      row_scales(w.k0, sr1);
+      row_scales(w.k0 + 1, sr2);
+    };
+    if (set > 0 && w.more()) w.next_tile();
+    if (w.more()) begin_tile();
+    for (; w.more() && ok; x_phase ^= 1) {
       const int n_eff = (d.nr + 15) & ~15;
-      float acc[NMAT][BN];
+      unsigned long long acc2[NMAT][BN / 2];
 #pragma unroll
       for (int m = 0; m < NMAT; ++m)
 #pragma unroll
-        for (int n = 0; n < BN; ++n) acc[m][n] = 0.0f;
-      const float* sw[NMAT];
-#pragma unroll
-      for (int m = 0; m < NMAT; ++m) sw[m] = fp8_weight_scales(p, m, d.slot, d.ft);
+        for (int n = 0; n < BN / 2; ++n) acc2[m][n] = 0ull;
       for (int kb = w.k0; kb < w.k1; ++kb, ++i) {
-        float sr[kGroups], ws[NMAT];   // lane j of group q holds the scale of token row 32 q + j
+        const int kj = (kb - w.k0) & 31;
+        if (kj == 0 && kb > w.k0) weight_scales(kb);
 #pragma unroll
-        for (int q = 0; q < kGroups; ++q)
-          sr[q] = q * 32 + lane < d.nr ? __ldg(p.sa + (d.rb + q * 32 + lane) * p.ld_sa + kb) : 0.0f;
-#pragma unroll
-        for (int m = 0; m < NMAT; ++m) ws[m] = __ldg(sw[m] + kb);
-        const int b = i % DB;
-        if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[b], (i / DB) & 1, kTagDFull, i, w.u)))) break;
+        for (int q = 0; q < kGroups; ++q) {
+          sr[q] = sr1[q];
+          sr1[q] = sr2[q];
+          if (BN >= 32 || lane < BN) sw[q * 32 + lane] = sr[q];
+        }
+        row_scales(kb + 2, sr2);
+        __syncwarp();   // the row scales stand in shared memory
+        const int b = set * DBS + i % DBS;
+        if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[b], (i / DBS) & 1, kTagDFull, i, w.u)))) break;
         tc_fence_after();
+        unsigned long long ws[NMAT];
+#pragma unroll
+        for (int m = 0; m < NMAT; ++m) {
+          const float v = __shfl_sync(0xFFFFFFFFu, wl[m], kj);
+          ws[m] = pack2(v, v);
+        }
         const uint32_t dcol = tmem + lane_base + b * NMAT * BN;
 #pragma unroll
         for (int c = 0; c < BN / 16; ++c) {
@@ -442,13 +506,19 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
           uint32_t v[NMAT][16];
 #pragma unroll
           for (int m = 0; m < NMAT; ++m) tmem_ld_32x32b_x16(dcol + m * BN + c * 16, v[m]);
+          float4 s4[4];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) s4[n] = *reinterpret_cast<const float4*>(sw + c * 16 + 4 * n);
           tmem_wait_ld();
 #pragma unroll
-          for (int n = 0; n < 16; ++n) {
-            const float s = __shfl_sync(0xFFFFFFFFu, sr[c / 2], (c & 1) * 16 + n);
+          for (int n = 0; n < 4; ++n) {
+            const unsigned long long lo = pack2(s4[n].x, s4[n].y), hi = pack2(s4[n].z, s4[n].w);
 #pragma unroll
-            for (int m = 0; m < NMAT; ++m)
-              acc[m][c * 16 + n] = fmaf(__uint_as_float(v[m][n]), s * ws[m], acc[m][c * 16 + n]);
+            for (int m = 0; m < NMAT; ++m) {
+              unsigned long long* a = &acc2[m][c * 8 + 2 * n];
+              fma2_to(a[0], v[m][4 * n], v[m][4 * n + 1], mul2(lo, ws[m]));
+              fma2_to(a[1], v[m][4 * n + 2], v[m][4 * n + 3], mul2(hi, ws[m]));
+            }
           }
         }
         tc_fence_before();
@@ -456,16 +526,32 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
         if (lane == 0) mbar_arrive(&d_empty[b]);
       }
       if (!ok) break;
+      const Fp8Unit done = d;
+      const long long u = w.u;
+      w.next_tile();
+      if (turns == 2) w.next_tile();
+      if (w.more()) begin_tile();
+      float acc[NMAT][BN];
+#pragma unroll
+      for (int m = 0; m < NMAT; ++m)
+#pragma unroll
+        for (int n = 0; n < BN / 2; ++n) {
+          const float2 f = unpack2(acc2[m][n]);
+          acc[m][2 * n] = f.x;
+          acc[m][2 * n + 1] = f.y;
+        }
       if (Cfg::kXBytes > 0 && S > 1) {
-        ok = S == 2   ? fp8_exchange<NMAT, BN, 2>(acc, xbuf, x_full, x_free, x_phase, rank, d.nr, row, lane, ab, w.u)
-             : S == 4 ? fp8_exchange<NMAT, BN, 4>(acc, xbuf, x_full, x_free, x_phase, rank, d.nr, row, lane, ab, w.u)
-                      : fp8_exchange<NMAT, BN, 8>(acc, xbuf, x_full, x_free, x_phase, rank, d.nr, row, lane, ab, w.u);
+        if (!joined) cluster_wait_all();
+        joined = true;
+        ok = S == 2   ? fp8_exchange<NMAT, BN, 2>(acc, xbuf, x_full, x_free, x_phase, rank, done.nr, row, lane, ab, u)
+             : S == 4 ? fp8_exchange<NMAT, BN, 4>(acc, xbuf, x_full, x_free, x_phase, rank, done.nr, row, lane, ab, u)
+                      : fp8_exchange<NMAT, BN, 8>(acc, xbuf, x_full, x_free, x_phase, rank, done.nr, row, lane, ab, u);
         if (!ok) break;
       }
       // this CTA's columns: token rows rb0 + j, j < nc
-      const int c0 = rank * (BN / S), nc = min(d.nr - c0, BN / S);
-      const long long rb0 = d.rb + c0;
-      const int feat = d.ft * 128 + row;
+      const int c0 = rank * (BN / S), nc = min(done.nr - c0, BN / S);
+      const long long rb0 = done.rb + c0;
+      const int feat = done.ft * 128 + row;
       if constexpr (NMAT == 1) {
         if (feat < p.N) {
           const size_t at = rb0 * p.ldo + feat;
@@ -497,13 +583,14 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
           const uint32_t m = max(max(tmax[j], tmax[BN + j]), max(tmax[2 * BN + j], tmax[3 * BN + j]));
           const Fp8Scale f = fp8_scale_of(__uint_as_float(m));
           if (feat < p.N) h[(rb0 + j) * p.ldo + feat] = uint8_t(cvt_e4m3x2(acc[0][j] * fp8_factor_of(f), 0.0f));
-          if (row == 0) p.hs[(rb0 + j) * hb + d.ft] = f.scale;
+          if (row == 0) p.hs[(rb0 + j) * hb + done.ft] = f.scale;
         }
         if (!(ok = epi.sync(lane))) break;   // the maxima are read before the next tile's are written
       }
     }
   }
   tc_fence_before();
+  if (S > 1 && !joined) cluster_wait_all();
   __syncthreads();
   if (S > 1) cluster_sync();   // no CTA leaves while another may still write to it
   pdl_launch_dependents();
@@ -524,6 +611,8 @@ constexpr int kFp8OutChunk = 128 * 128;   // staged output: 128 rows of 128 byte
 template <int NMAT, bool PAIR>
 struct Fp8TileCfg {
   static constexpr int kRows = PAIR ? 256 : 128;                // token rows a tile
+  // columns the epilogue reads at once
+  static constexpr int kChunk = !PAIR && NMAT == 1 ? 16 : 32;
   static constexpr int kWRows = PAIR ? 128 : 256;               // weight rows this CTA loads
   static constexpr int kStages = PAIR || NMAT == 2 ? 4 : 3;
   static constexpr int kStageBytes = kFp8WBytes + kWRows * 128;
@@ -533,10 +622,6 @@ struct Fp8TileCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 constexpr int kFp8TileThreads = 384;   // warps for TMA, MMA, output stores and waiting; two epilogue warpgroups
-
-__device__ __forceinline__ void fma2_to(unsigned long long& acc, uint32_t lo, uint32_t hi, unsigned long long s) {
-  acc = fma2(pack2(__uint_as_float(lo), __uint_as_float(hi)), s, acc);
-}
 
 // An arrive on a barrier of the pair.  It says only that this warp's tensor
 // memory loads are done (they are waited for); a release at cluster scope
@@ -603,7 +688,24 @@ __device__ __forceinline__ void tma_store_2d(const void* map, const void* src, i
                ::"l"(map), "r"(smem_u32(src)), "r"(x), "r"(y) : "memory");
 }
 
-template <int NMAT, bool PAIR>
+// Staged rows to an output without a tensor map, an element a lane.
+__device__ __forceinline__ void fp8_store_rows(uint8_t* dst, long long pitch, const uint8_t* rows, int n, int nf, int esize,
+                                            int lane) {
+#pragma unroll 2
+  for (int r = 0; r < n; ++r, dst += pitch) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int f = lane + 32 * q, byte = f * esize;   // of the row's 256 staged bytes
+      if (f >= nf) continue;
+      const uint8_t* src = rows + (byte >> 7) * kFp8OutChunk + r * 128 + ((((byte >> 4) & 7) ^ (r & 7)) << 4) + (byte & 15);
+      if (esize == 4) reinterpret_cast<uint32_t*>(dst)[f] = *reinterpret_cast<const uint32_t*>(src);
+      else reinterpret_cast<uint16_t*>(dst)[f] = *reinterpret_cast<const uint16_t*>(src);
+    }
+  }
+}
+
+// TMA_OUT: the output has a tensor map (a kernel without one has registers spilled by the plain stores).
+template <int NMAT, bool PAIR, bool TMA_OUT>
 __global__ void __launch_bounds__(kFp8TileThreads, 1)
 fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
                 const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_rows,
@@ -756,43 +858,35 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
           if (++s == NST) { s = 0; phase ^= 1; }
         }
       }
-    } else if (warp == 2 && NMAT == 1) {
+    } else if (warp == 2 && NMAT == 1 && TMA_OUT) {
       // -------------------------------------------- output stores ---
       // The staged features of each half (128 bf16; or 64 fp32, twice), as
       // 32-row boxes of 128 bytes, behind the next tile's sums: stores from the
       // epilogue warps themselves held them, and with them the MMAs, for a
-      // quarter of the time.  A box that would reach past the group's rows, and
-      // an output without a tensor map, goes by plain stores.
+      // quarter of the time.  The rows of a box that would reach past the
+      // group's go by 16-byte stores.
       const bool f32 = p.out_type == FT_F32;
       const int esize = f32 ? 4 : 2, per = 128 / esize;   // features a chunk
       uint32_t n = 0;
       bool ok = true;
       for (int u = u0; u < n_units && ok; u += du) {
         const Fp8Unit d = fp8_unit(p, u, Cfg::kRows);
-        const int rb = d.rb + rank * 128, nr = max(0, min(d.nr - int(rank) * 128, 128));
+        const int rb = d.rb + rank * 128, nr = max(0, min(d.nr - int(rank) * 128, 128)), boxes = nr / 32;
         for (int pass = 0; pass < (f32 ? 2 : 1) && ok; ++pass, ++n) {
           for (int half = 0; half < 2; ++half) {
             if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&out_full[half], n & 1, kTagOut, n, u)))) break;
+#pragma unroll 1
             for (int c = 0; c < 2; ++c) {
               const uint8_t* stage = out_stage + (half * 2 + c) * kFp8OutChunk;
               const int f0 = d.ft * 256 + half * 128 + (2 * pass + c) * per, nf = min(per, p.N - f0);
-              const int boxes = p.out_tma ? nr / 32 : 0;
               if (nf <= 0) break;
               if (lane < boxes) tma_store_2d(&tm_out, stage + lane * 32 * 128, f0, rb + lane * 32);
+#pragma unroll 1
               for (int row = boxes * 32 + (lane >> 3); row < nr; row += 4) {
-                const int piece = lane & 7;
+                const int piece = lane & 7, f = piece * (16 / esize);
                 const uint4 x = *reinterpret_cast<const uint4*>(stage + row * 128 + ((piece ^ (row & 7)) << 4));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                const int f = piece * (16 / esize);
                 uint8_t* dst = static_cast<uint8_t*>(p.out) + ((rb + row) * p.ldo + f0 + f) * esize;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  if (f32) {
-                    if (e < 4 && f + e < nf) reinterpret_cast<uint32_t*>(dst)[e] = w[e & 3];
-                  } else if (f + e < nf) {
-                    reinterpret_cast<uint16_t*>(dst)[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
-                  }
-                }
+                if (f < nf) *reinterpret_cast<uint4*>(dst) = x;   // N ends on a piece
               }
             }
             asm volatile("cp.async.bulk.commit_group;\n cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -816,6 +910,7 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
     uint32_t i = 0, staged = 0;
     bool ok = true;
     int parity = 0;
+    constexpr int kCh = Cfg::kChunk, kNc = 128 / kCh;
     // A tile's descriptor and its first two blocks' scales are fetched behind
     // the tile before it: two dependent round trips to memory.
     Fp8Unit d = {};
@@ -841,19 +936,19 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
       fetch_scales();
     }
     for (int u = u0; u < n_units && ok; u += du, parity ^= 1) {
-      const int rb = d.rb + rank * 128;
-      const bool live = int(rank) * 128 + row < d.nr;
+      const int rb = d.rb + rank * 128, nr_here = d.nr - int(rank) * 128;
+      const bool live = row < nr_here;
       unsigned long long acc[64];   // NMAT 1: 128 columns; NMAT 2: gate of 64 features, then up
 #pragma unroll
       for (int c = 0; c < 64; ++c) acc[c] = 0ull;
-      // Chunks of 32 columns in two register buffers, the next chunk's load in
+      // Chunks of kCh columns in two register buffers, the next chunk's load in
       // flight behind one chunk's sums -- also across blocks: the last chunk's
       // sums stand behind the next block's first load.
-      uint32_t v[2][32];
+      uint32_t v[2][kCh];
       if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[2 * (i & 1) + half], (i >> 1) & 1, kTagDFull, i, u)))) break;
       tc_fence_after();
       const uint32_t dcol = tmem + lane_base + half * 128;
-      tmem_ld_32x32b_x32(dcol + (i & 1) * 256, v[0]);
+      tmem_ld_cols(dcol + (i & 1) * 256, v[0]);
       for (int kb = 0; kb < nk; ++kb, ++i) {
         const uint32_t b = i & 1;
         const float s0 = a * w0, s1 = a * w1;
@@ -869,13 +964,14 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
         bool ready = false;
         auto sums = [&](int c) {
 #pragma unroll
-          for (int n = 0; n < 16; ++n) fma2_to(acc[c * 16 + n], v[c & 1][2 * n], v[c & 1][2 * n + 1], c < 2 ? p0 : p1);
+          for (int n = 0; n < kCh / 2; ++n)
+            fma2_to(acc[c * (kCh / 2) + n], v[c & 1][2 * n], v[c & 1][2 * n + 1], c < kNc / 2 ? p0 : p1);
         };
 #pragma unroll
-        for (int c = 0; c < 3; ++c) {
+        for (int c = 0; c < kNc - 1; ++c) {
           tmem_wait_ld();
-          tmem_ld_32x32b_x32(dcol + b * 256 + (c + 1) * 32, v[(c + 1) & 1]);
-          if (c == 2) ready = mbar_test_wait(&d_full[2 * (b ^ 1) + half], ((i + 1) >> 1) & 1);
+          tmem_ld_cols(dcol + b * 256 + (c + 1) * kCh, v[(c + 1) & 1]);
+          if (c == kNc - 2) ready = mbar_test_wait(&d_full[2 * (b ^ 1) + half], ((i + 1) >> 1) & 1);
           sums(c);
         }
         tmem_wait_ld();
@@ -886,16 +982,16 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
           else mbar_arrive(&d_empty[2 * b + half]);
         }
         if (kb == last) {
-          sums(3);
+          sums(kNc - 1);
         } else {
           if (!ready) {
-            sums(3);
+            sums(kNc - 1);
             if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[2 * (b ^ 1) + half], ((i + 1) >> 1) & 1, kTagDFull, i + 1, u))))
               break;
           }
           tc_fence_after();
-          tmem_ld_32x32b_x32(dcol + (b ^ 1) * 256, v[0]);
-          if (ready) sums(3);
+          tmem_ld_cols(dcol + (b ^ 1) * 256, v[0]);
+          if (ready) sums(kNc - 1);
         }
       }
       if (!ok) break;
@@ -905,11 +1001,12 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
         // each thread its row's features, to the store warp: 16-byte piece q of a row at q ^ (row % 8)
         uint8_t* stage = out_stage + half * 2 * kFp8OutChunk + row * 128;
         const bool f32 = p.out_type == FT_F32;
-#pragma unroll
-        for (int pass = 0; pass < 2; ++pass) {
-          if (pass == 1 && !f32) break;
-          if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&out_empty[half], (staged & 1) ^ 1, kTagOut, staged, u)))) break;
-          ++staged;
+        auto give = [&](auto pass_tag) {   // the accumulators' indices have to be constants
+          constexpr int pass = decltype(pass_tag)::value;
+          if constexpr (TMA_OUT) {
+            if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&out_empty[half], (staged & 1) ^ 1, kTagOut, staged, u)))) return;
+            ++staged;
+          }
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
             uint32_t o[4];
@@ -928,10 +1025,21 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
             *reinterpret_cast<uint4*>(stage + (q >> 3) * kFp8OutChunk + (((q & 7) ^ (row & 7)) << 4)) =
                 make_uint4(o[0], o[1], o[2], o[3]);
           }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&out_full[half]);
-        }
+          if constexpr (TMA_OUT) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&out_full[half]);
+          } else {
+            __syncwarp();
+            const int esize = f32 ? 4 : 2, f0 = ft * 256 + half * 128 + pass * 64;
+            fp8_store_rows(static_cast<uint8_t*>(p.out) + ((long long)(rb + quarter * 32) * p.ldo + f0) * esize,
+                           p.ldo * esize, out_stage + half * 2 * kFp8OutChunk + quarter * 32 * 128,
+                           min(32, nr_here - quarter * 32), min(256 / esize, p.N - f0), esize, lane);
+            __syncwarp();
+          }
+        };
+        give(std::integral_constant<int, 0>());
+        if (f32 && ok) give(std::integral_constant<int, 1>());
         fetch_scales();
         if (!ok) break;
       } else {
@@ -999,7 +1107,7 @@ __global__ void __launch_bounds__(256) fp8_prep_kernel(const Fp8PrepParams p) {
     return;
   }
   const int H = p.sched.H;
-  const uint32_t nb = (H + kFp8Block - 1) / kFp8Block, groups = uint32_t(p.sched.P) * nb;   // T k <= 2^24, nb <= 512
+  const uint32_t nb = (H + kFp8Block - 1) / kFp8Block, groups = uint32_t(p.sched.P) * nb;   // < 2^31
   const uint32_t block = blockIdx.x - p.sched.nsched, stride = (gridDim.x - p.sched.nsched) * 32u;
   const int sub = threadIdx.x & 7;
   Raw16<__nv_bfloat16> raw;
@@ -1032,6 +1140,40 @@ __global__ void __launch_bounds__(256) fp8_prep_kernel(const Fp8PrepParams p) {
   }
 }
 
+// The rows of x, already quantised once a token, to their places in expert
+// order: a warp a row.  Bound by the writes of k copies.  The kernel above does
+// a token's arithmetic k times instead: at 4096 tokens x 2048, k = 8, the FFN
+// takes 277 us with it and 268 with these two launches (1500 tokens x 2880,
+// k = 4: the same within the noise).
+struct Fp8SpreadParams {
+  PrepParams sched;
+  int T;
+  const uint8_t* from_codes;   // [T, H]
+  const float* from_scales;    // [T, ceil(H/128)]
+  uint8_t* codes;              // [P, H]
+  float* scales;
+};
+__global__ void __launch_bounds__(256) fp8_spread_kernel(const Fp8SpreadParams p) {
+  pdl_enter();
+  if (int(blockIdx.x) < p.sched.nsched) {
+    prep_schedule(p.sched, blockIdx.x);
+    return;
+  }
+  const int lane = threadIdx.x & 31, H = p.sched.H, nb = (H + kFp8Block - 1) / kFp8Block;
+  const int stride = (gridDim.x - p.sched.nsched) * 8;
+  for (int r = (blockIdx.x - p.sched.nsched) * 8 + (threadIdx.x >> 5); r < p.sched.P; r += stride) {
+    const int src = __ldg(p.sched.perm_src + r), t = src / p.sched.k_top;
+    const bool known = src >= 0 && t < p.T;
+    if (!known && lane == 0) set_device_status(FT_DEV_BAD_INDEX);
+    const uint4* from = reinterpret_cast<const uint4*>(p.from_codes + (long long)t * H);   // H is a multiple of 64
+    uint4* to = reinterpret_cast<uint4*>(p.codes + (long long)r * H);
+#pragma unroll 4
+    for (int c = lane; c < H / 16; c += 32) to[c] = known ? __ldg(from + c) : make_uint4(0u, 0u, 0u, 0u);
+    for (int c = lane; c < nb; c += 32)
+      p.scales[(long long)r * nb + c] = known ? __ldg(p.from_scales + (long long)t * nb + c) : 0.0f;
+  }
+}
+
 // ---------------------------------------------------------------- host ---
 
 // Codes [rows, K] (pitch bytes) as boxes of 128 K x box_rows, 128-byte swizzle.
@@ -1048,11 +1190,13 @@ static bool make_fp8_map(const void* base, long long rows, int K, long long pitc
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The output [rows, N] as boxes of 32 rows x 128 bytes; false where its pitch or address does not allow a map.
+// The output [rows, N] as boxes of 32 rows x 128 bytes; false where its pitch
+// or address does not allow a map, or a row does not end on 16 bytes (a store
+// cuts its box there: with N = 333 fp32 columns it wrote zeros to 333 .. 335).
 static bool make_fp8_out_map(void* out, int out_type, long long rows, int N, long long ldo, CUtensorMap* m) {
   auto enc = tensor_map_encoder();
   const int esize = out_type == FT_F32 ? 4 : 2;
-  if (!enc || (ldo * esize) % 16 || (reinterpret_cast<uintptr_t>(out) & 15)) return false;
+  if (!enc || (ldo * esize) % 16 || (N * esize) % 16 || (reinterpret_cast<uintptr_t>(out) & 15)) return false;
   const cuuint64_t dims[2] = {cuuint64_t(N), cuuint64_t(rows)};
   const cuuint64_t strides[1] = {cuuint64_t(ldo * esize)};
   const cuuint32_t box[2] = {cuuint32_t(128 / esize), 32};
@@ -1135,21 +1279,21 @@ static cudaError_t launch_fp8_stream(Fp8Params p, double units, long long most, 
   for (int i = 1; Cfg::kXBytes > 0 && i < 4 && (1 << i) <= p.nk; ++i) {
     const int S = 1 << i, per = (p.nk + S - 1) / S;
     if ((S - 1) * per >= p.nk) continue;   // a CTA without a block
-    const int n = fp8_cluster_ctas(kern, kFp8StreamThreads, kMost, S, num_sms, &ctas[dev][i]);
+    const int n = fp8_cluster_ctas(kern, Cfg::kThreads, kMost, S, num_sms, &ctas[dev][i]);
     const double cost = ceil(units / (n / S)) * (per + 3);
     if (cost < best - 1e-9) { best = cost; p.split = S; cap = n; }
   }
   const int grid = int(std::min<long long>(most * p.split, cap));
-  return launch_fp8_grid(kern, grid, kFp8StreamThreads, Cfg::smem_bytes(p.E), p.split, s, p, w0, w1, rows);
+  return launch_fp8_grid(kern, grid, Cfg::kThreads, Cfg::smem_bytes(p.E), p.split, s, p, w0, w1, rows);
 }
 static int fp8_tile_grid(long long units, bool pair, int num_sms) {
   return pair ? 2 * int(std::min<long long>(units, num_sms / 2)) : int(std::min<long long>(units, num_sms));
 }
-template <int NMAT, bool PAIR>
+template <int NMAT, bool PAIR, bool TMA_OUT>
 static cudaError_t launch_fp8_tile(const Fp8Params& p, long long units, int num_sms, const CUtensorMap& w0,
                                    const CUtensorMap& w1, const CUtensorMap& rows, const CUtensorMap& out, cudaStream_t s) {
   static std::atomic<uint64_t> done[64];
-  auto kern = fp8_tile_kernel<NMAT, PAIR>;
+  auto kern = fp8_tile_kernel<NMAT, PAIR, TMA_OUT>;
   constexpr int kSmem = Fp8TileCfg<NMAT, PAIR>::kSmemBytes;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1168,13 +1312,17 @@ static cudaError_t launch_fp8_any(int bn, Fp8Params p, long long out_rows, doubl
                                   const CUtensorMap& w0, const CUtensorMap& w1, const CUtensorMap& rows, cudaStream_t s) {
   const int num_sms = device_sm_count();
   CUtensorMap out = rows;
-  if (bn >= 128 && NMAT == 1) p.out_tma = make_fp8_out_map(p.out, p.out_type, out_rows, p.N, p.ldo, &out);
+  const bool mapped = bn < 128 || NMAT == 2 || make_fp8_out_map(p.out, p.out_type, out_rows, p.N, p.ldo, &out);
   switch (bn) {
     case 16: return launch_fp8_stream<NMAT, 16>(p, units, most, num_sms, w0, w1, rows, s);
     case 32: return launch_fp8_stream<NMAT, 32>(p, units, most, num_sms, w0, w1, rows, s);
     case 64: return launch_fp8_stream<NMAT, 64>(p, units, most, num_sms, w0, w1, rows, s);
-    case 128: return launch_fp8_tile<NMAT, false>(p, most, num_sms, w0, w1, rows, out, s);
-    default: return launch_fp8_tile<NMAT, true>(p, most, num_sms, w0, w1, rows, out, s);
+    case 128:   // experts: H is a multiple of 64, every output has a map
+      return mapped ? launch_fp8_tile<NMAT, false, true>(p, most, num_sms, w0, w1, rows, out, s) : cudaErrorInvalidValue;
+    default:
+      if constexpr (NMAT == 1)
+        if (!mapped) return launch_fp8_tile<NMAT, true, false>(p, most, num_sms, w0, w1, rows, out, s);
+      return launch_fp8_tile<NMAT, true, true>(p, most, num_sms, w0, w1, rows, out, s);
   }
 }
 
@@ -1188,8 +1336,8 @@ static double fp8_padded(double mean, int b) {
 // kernel on one CTA or a pair).  For few rows a quarter more than the mean, so
 // that most groups of an even spread are one tile.  A pair takes 0.9 of the
 // time for the same padded rows (32 groups of some 187 rows, two or one tile
-// each: the FFN 241 us against 270) but pads more (4096 skewed tokens of
-// 128 groups: 316 us against 277).
+// each: the FFN 249 us against 268) but pads more (4096 skewed tokens of
+// 128 groups: 317 us against 277).
 static int fp8_rows_tile(double mean) {
   const double rows = 1.25 * mean;
   if (rows <= 64) return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
@@ -1204,10 +1352,15 @@ static int fp8_weight_box(int bn, int nmat) {
 struct Fp8GemmPlan {
   int bn, row_tiles, feat_tiles;
 };
+// The stream kernel while one tile takes all rows, or while its tiles are no
+// more than the SMs (65 x 1024 x 2048: 7.6 us against 10.5 of the tile kernel,
+// 200 x 2048 x 2048: 9.9 against 11.0); past that its CTAs take a second tile
+// (128 x 8192 x 2048: 15.9 us against 11.5, 64 x 16384 x 2048: 15.9 against
+// 11.4) and each reads the weights again.
 static Fp8GemmPlan plan_fp8_gemm(int M, int N, int num_sms) {
   Fp8GemmPlan pl{};
-  const long long big = ((M + 127LL) / 128) * ((N + 255LL) / 256);
-  pl.bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 || big * 2 < num_sms ? 64 : M > 512 ? 256 : 128;
+  const long long jobs = ((M + 31LL) / 32) * ((N + 127LL) / 128);
+  pl.bn = M <= 16 ? 16 : (M <= 32 || jobs <= num_sms) ? 32 : 256;
   pl.row_tiles = (M + pl.bn - 1) / pl.bn;
   pl.feat_tiles = pl.bn >= 128 ? (N + 255) / 256 : (N + 127) / 128;
   return pl;
@@ -1246,7 +1399,8 @@ struct Fp8FfnPlan {
   int bn, mt1, mt2;                 // token rows a tile takes; feature tiles of gate/up and down
   double tiles;                     // token tiles, as far as the host can tell
   long long max_units1, max_units2;
-  size_t off_x, off_xs, off_h, off_hs, off_units1, off_units2, off_counts, total;
+  bool spread;                      // quantise by token, then copy to the rows
+  size_t off_x, off_xs, off_h, off_hs, off_t, off_ts, off_units1, off_units2, off_counts, total;
 };
 static Fp8FfnPlan plan_fp8_ffn(int T, int H, int I, int E, int k) {
   Fp8FfnPlan p{};
@@ -1265,6 +1419,9 @@ static Fp8FfnPlan plan_fp8_ffn(int T, int H, int I, int E, int k) {
   p.off_xs = o;     o = align256(o + size_t(P) * fp8_blocks(H) * 4);
   p.off_h = o;      o = align256(o + size_t(P) * I);
   p.off_hs = o;     o = align256(o + size_t(P) * fp8_blocks(I) * 4);
+  p.spread = !stream && k > 1;
+  p.off_t = o;      o = align256(o + (p.spread ? size_t(T) * H : 0));
+  p.off_ts = o;     o = align256(o + (p.spread ? size_t(T) * fp8_blocks(H) * 4 : 0));
   p.off_units1 = o; o = align256(o + (stream ? 0 : size_t(p.max_units1) * 16));
   p.off_units2 = o; o = align256(o + (stream ? 0 : size_t(p.max_units2) * 16));
   p.off_counts = o; o = align256(o + 16);
@@ -1296,26 +1453,40 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
   int4* units2 = reinterpret_cast<int4*>(w + pl.off_units2);
   int* counts = reinterpret_cast<int*>(w + pl.off_counts);
   cudaError_t e;
-  {
+  PrepParams sp{};
+  sp.offsets = offsets;
+  sp.slot_table = slot_table;
+  sp.E = E;
+  sp.num_slots = L.num_slots;
+  // the stream kernel finds its tiles itself
+  sp.nsched = stream ? 0 : int(std::min<long long>(32, std::max<long long>(1, (pl.max_units1 + pl.max_units2) / 4096)));
+  sp.bn1 = sp.bn2 = pl.bn;
+  sp.mt1 = pl.mt1;
+  sp.mt2 = pl.mt2;
+  sp.s1 = sp.s2 = 1;
+  sp.units1 = units1;
+  sp.units2 = units2;
+  sp.counts = counts;
+  sp.perm_src = perm_src;
+  sp.P = P;
+  sp.k_top = k;
+  sp.H = H;
+  if (pl.spread) {
+    Fp8SpreadParams pp{};
+    pp.sched = sp;
+    pp.T = T;
+    pp.from_codes = w + pl.off_t;
+    pp.from_scales = reinterpret_cast<const float*>(w + pl.off_ts);
+    pp.codes = w + pl.off_x;
+    pp.scales = reinterpret_cast<float*>(w + pl.off_xs);
+    e = launch_fp8_quant(x, FT_BF16, T, H, H, w + pl.off_t, H, reinterpret_cast<float*>(w + pl.off_ts), fp8_blocks(H), s);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min((P + 7) / 8, device_sm_count() * 8);
+    ProfileScope prof(FT_KERNEL_PREP, s);
+    e = launch_pdl(fp8_spread_kernel, dim3(sp.nsched + ctas), dim3(256), 0, s, pp);
+  } else {
     Fp8PrepParams pp{};
-    PrepParams& sp = pp.sched;
-    sp.offsets = offsets;
-    sp.slot_table = slot_table;
-    sp.E = E;
-    sp.num_slots = L.num_slots;
-    // the stream kernel finds its tiles itself
-    sp.nsched = stream ? 0 : int(std::min<long long>(32, std::max<long long>(1, (pl.max_units1 + pl.max_units2) / 4096)));
-    sp.bn1 = sp.bn2 = pl.bn;
-    sp.mt1 = pl.mt1;
-    sp.mt2 = pl.mt2;
-    sp.s1 = sp.s2 = 1;
-    sp.units1 = units1;
-    sp.units2 = units2;
-    sp.counts = counts;
-    sp.perm_src = perm_src;
-    sp.P = P;
-    sp.k_top = k;
-    sp.H = H;
+    pp.sched = sp;
     pp.x = static_cast<const __nv_bfloat16*>(x);
     pp.T = T;
     pp.codes = w + pl.off_x;

@@ -138,3 +138,13 @@ def test_python_refusals():
                  lambda: fp8.Fp8Linear(x, torch.zeros(1, 1))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_ffn_refuses_more_blocks_than_32_bits_count(L):
+    H = 65536      # 512 blocks a row
+    lay = _lib.slot_layout(H, 256, 8, _lib.FT_SCALE_FP8)
+    for T in (1 << 22, 1 << 23):
+        assert ffn(L, lay, T=T, H=H, I=256, k=1) == _lib.FT_ERR_UNSUPPORTED
+        assert _lib.ffn_fp8_workspace_size(T, H, 256, 8, 1) == 0
+        assert _lib.ffn_fp8_workspace_size(T, 256, H, 8, 1) == 0
+    assert _lib.ffn_fp8_workspace_size((1 << 22) - 1, H, 256, 8, 1) > 0
