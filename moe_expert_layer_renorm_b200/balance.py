@@ -33,7 +33,9 @@ class RouterBalance:
         assert ids.dtype == torch.int32 and ids.shape == (self.T, self.k) and ids.is_contiguous()
         assert valid is None or (valid.dtype in (torch.bool, torch.uint8) and valid.shape == (self.T,) and
                                  valid.is_contiguous())
-        assert logits.device.index == torch.cuda.current_device(), "the tensors are not on the current device"
+        here = torch.cuda.current_device()
+        assert logits.get_device() == here and self.counts.get_device() == here and ids.get_device() == here and \
+            (valid is None or valid.get_device() == here), "a tensor is not on the current device"
 
     def _pitch(self, t: torch.Tensor) -> int:
         return t.stride(0) if self.T > 1 else max(t.stride(0), self.E)
@@ -53,10 +55,12 @@ class RouterBalance:
         """dlogits of the last forward()'s loss (times dloss, fp32 [1]; None: 1), plus that of the router's
         weights w with the gradient dw (both fp32 [T, k]) where they are given."""
         self._check(logits, ids, valid)
-        assert dloss is None or (dloss.dtype == torch.float32 and dloss.numel() == 1)
+        assert dloss is None or (dloss.dtype == torch.float32 and dloss.numel() == 1 and
+                                 dloss.get_device() == logits.get_device())
         assert (w is None) == (dw is None)
         for t in (w, dw):
-            assert t is None or (t.dtype == torch.float32 and t.shape == (self.T, self.k) and t.is_contiguous())
+            assert t is None or (t.dtype == torch.float32 and t.shape == (self.T, self.k) and t.is_contiguous() and
+                                 t.get_device() == logits.get_device())
         _lib.route_backward(logits.data_ptr(), self._pitch(logits), ids.data_ptr(), _ptr(w), _ptr(dw), _ptr(valid),
                             self.T, self.E, self.k, self.coef, self.counts.data_ptr(), self.n_valid.data_ptr(),
                             _ptr(dloss), self.dlogits.data_ptr(), self.E, _stream(stream))

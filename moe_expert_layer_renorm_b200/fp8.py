@@ -4,10 +4,12 @@ product: torch buffers around ft_fp8_quant_rows, ft_fp8_pack and ft_fp8_gemm.
 Codes are torch.float8_e4m3fn tensors [rows, K] whose rows start on 16 bytes
 (a view of wider rows where K is not a multiple of 16); scales are fp32.
 Every call is enqueued on ``stream`` (default: the current one) of the current
-device, which has to be the tensors' own.
+device, which has to be the tensors' own; the tensors that it returns are
+allocated on that stream.
 """
 from __future__ import annotations
 
+import contextlib
 from typing import Optional, Tuple
 
 import torch
@@ -26,6 +28,11 @@ def _blocks(n: int) -> int:
 def _here(t: torch.Tensor) -> None:
     if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {t.device}, which is not the current device")
+
+
+def _allocating(stream):
+    """New tensors belong to `stream`: one of the current stream's could still be in use there."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def empty_codes(rows: int, K: int, device) -> torch.Tensor:
@@ -63,10 +70,12 @@ def quantize_rows(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales:
     _here(x)
     M, K = x.shape
     given = codes is not None or scales is not None
-    if codes is None:
-        codes = empty_codes(M, K, x.device)
-    if scales is None:
-        scales = torch.empty((M, (K + 127) // 128), dtype=torch.float32, device=x.device)
+    if codes is None or scales is None:
+        with _allocating(stream):
+            if codes is None:
+                codes = empty_codes(M, K, x.device)
+            if scales is None:
+                scales = torch.empty((M, (K + 127) // 128), dtype=torch.float32, device=x.device)
     if given:
         _check_codes(codes, scales, M, "quantize_rows")
         if codes.shape != (M, K) or codes.get_device() != x.get_device():
@@ -82,8 +91,9 @@ def pack_weight(w: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tenso
         raise ValueError("pack_weight: w must be a contiguous fp32 CUDA matrix")
     _here(w)
     N, K = w.shape
-    codes = empty_codes(N, K, w.device)
-    scales = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
+    with _allocating(stream):
+        codes = empty_codes(N, K, w.device)
+        scales = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=w.device)
     _lib.fp8_pack(w.data_ptr(), N, K, codes.data_ptr(), _code_pitch(codes), scales.data_ptr(), scales.shape[1],
                   _stream(stream))
     return codes, scales
@@ -113,7 +123,8 @@ class Fp8Linear:
         if out is None:
             if out_dtype not in (torch.bfloat16, torch.float32):
                 raise ValueError("matmul: out_dtype must be bf16 or fp32")
-            out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+            with _allocating(stream):
+                out = torch.empty((M, N), dtype=out_dtype, device=a.device)
         elif out.shape != (M, N) or out.dtype not in (torch.bfloat16, torch.float32) or \
                 out.get_device() != a.get_device() or (N > 1 and out.stride(1) != 1):
             raise ValueError("matmul: out must be bf16 or fp32 [M, N] with contiguous rows, on the rows' device")
@@ -126,8 +137,4 @@ class Fp8Linear:
     def forward(self, x: torch.Tensor, out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """x [M, K] (fp32, bf16 or fp16) -> x W^T: its rows to FP8, then the product."""
         codes, scales = quantize_rows(x, stream=stream)
-        y = self.matmul(codes, scales, out_dtype=out_dtype, stream=stream)
-        if stream is not None:
-            codes.record_stream(stream)
-            scales.record_stream(stream)
-        return y
+        return self.matmul(codes, scales, out_dtype=out_dtype, stream=stream)

@@ -48,6 +48,8 @@ class ExpertPool:
         self.slot_bytes = int(self.layout.slot_bytes)
         if buf is None:
             buf = torch.zeros(num_slots * self.slot_bytes, dtype=torch.uint8, device=device)
+        else:
+            assert buf.is_cuda and buf.data_ptr() % 256 == 0
         assert buf.dtype == torch.uint8 and buf.is_contiguous() and buf.numel() == num_slots * self.slot_bytes
         self.buf = buf
         self._pack_ws = torch.zeros(256, dtype=torch.uint8, device=buf.device)

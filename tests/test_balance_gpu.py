@@ -172,3 +172,15 @@ def test_router_step_lowers_a_skewed_loss_with_the_router_kernel():
     up, down = float(b.forward(l + step, ids)), float(b.forward(l - step, ids))
     # the third-order term of a step of 0.05 is a few 1e-3 of the first; the loss itself is good to 1e-6
     assert (up - down) / 2 == pytest.approx(float((d * step).sum()), rel=2e-2, abs=2e-6)
+
+
+def test_tensors_of_another_device_are_refused():
+    b = RouterBalance(4, 8, 2, 0.01)
+    logits, ids, w = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, 2)
+    valid, one = torch.ones(4, dtype=torch.bool), torch.ones(1)
+    L, I, W = logits.cuda(), ids.cuda(), w.cuda()
+    for call in (lambda: b.forward(logits, I), lambda: b.forward(L, ids), lambda: b.forward(L, I, valid),
+                 lambda: b.backward(L, I, dloss=one), lambda: b.backward(L, I, w=w, dw=W),
+                 lambda: b.backward(L, I, w=W, dw=w)):
+        with pytest.raises(AssertionError):
+            call()

@@ -264,6 +264,33 @@ FFN_SHAPES = [
     ([700, 0], 512, 256, 2), ([257, 255, 100, 513], 320, 448, 3), ([140, 90, 130], 256, 512, 1), ([1, 1, 1, 1, 1, 1, 1, 1], 2048, 768, 8), ([3, 2], 2880, 2880, 1), ([90, 160], 576, 2880, 2)]
 
 
+def test_results_on_a_given_stream_are_not_memory_the_current_one_still_writes():
+    M, N, K = 512, 1024, 4096
+    x = torch.randn(M, K, device="cuda")
+    lin = fp8.Fp8Linear.from_weight(torch.randn(N, K, device="cuda"))
+    codes, scales = fp8.quantize_rows(x)
+    want = lin.matmul(codes, scales)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def after_a_late_fill(call, *shapes):
+        held = [torch.empty(s, dtype=t, device="cuda") for s, t in shapes]
+        torch.cuda._sleep(20_000_000)      # some 10 ms, then the current stream writes what it has given back
+        for h in held:
+            h.view(torch.uint8).fill_(0x2A)
+        del held, h
+        got = call()
+        torch.cuda.synchronize()
+        return got
+
+    got = after_a_late_fill(lambda: fp8.quantize_rows(x, stream=side), ((M, K), fp8.FP8), ((M, K // 128), torch.float32))
+    assert np.array_equal(_u8(got[0]), _u8(codes)) and torch.equal(got[1], scales)
+    got = after_a_late_fill(lambda: lin.matmul(codes, scales, stream=side), ((M, N), torch.bfloat16))
+    assert torch.equal(got, want)
+    got = after_a_late_fill(lambda: lin.forward(x, stream=side), ((M, K), fp8.FP8), ((M, N), torch.bfloat16))
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("out", ["fp32", "bf16"])
 @pytest.mark.parametrize("rows,H,I,k", FFN_SHAPES)
 def test_ffn(rows, H, I, k, out):
