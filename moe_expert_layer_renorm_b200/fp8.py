@@ -69,17 +69,25 @@ def quantize_rows(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales:
         raise ValueError("quantize_rows: x must be a CUDA matrix of fp32, bf16 or fp16 with contiguous rows")
     _here(x)
     M, K = x.shape
-    given = codes is not None or scales is not None
+    if codes is None and scales is None:     # the usual call: nothing of theirs to look up again
+        pitch, blocks = (K + 15) // 16 * 16, (K + 127) // 128
+        if stream is None:
+            wide, scales = x.new_empty((M, pitch), dtype=FP8), x.new_empty((M, blocks), dtype=torch.float32)
+        else:
+            with _allocating(stream):
+                wide, scales = x.new_empty((M, pitch), dtype=FP8), x.new_empty((M, blocks), dtype=torch.float32)
+        _lib.fp8_quant_rows(x.data_ptr(), kind, M, K, _pitch(x), wide.data_ptr(), pitch, scales.data_ptr(), blocks,
+                            _stream(stream))
+        return (wide if pitch == K else wide[:, :K]), scales
     if codes is None or scales is None:
         with _allocating(stream):
             if codes is None:
                 codes = empty_codes(M, K, x.device)
             if scales is None:
-                scales = torch.empty((M, (K + 127) // 128), dtype=torch.float32, device=x.device)
-    if given:
-        _check_codes(codes, scales, M, "quantize_rows")
-        if codes.shape != (M, K) or codes.get_device() != x.get_device():
-            raise ValueError("quantize_rows: codes must have x's shape and device")
+                scales = torch.empty((M, _blocks(K)), dtype=torch.float32, device=x.device)
+    _check_codes(codes, scales, M, "quantize_rows")
+    if codes.shape != (M, K) or codes.get_device() != x.get_device():
+        raise ValueError("quantize_rows: codes must have x's shape and device")
     _lib.fp8_quant_rows(x.data_ptr(), kind, M, K, _pitch(x), codes.data_ptr(), _code_pitch(codes), scales.data_ptr(),
                         _pitch(scales), _stream(stream))
     return codes, scales
@@ -123,8 +131,11 @@ class Fp8Linear:
         if out is None:
             if out_dtype not in (torch.bfloat16, torch.float32):
                 raise ValueError("matmul: out_dtype must be bf16 or fp32")
-            with _allocating(stream):
-                out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+            if stream is None:
+                out = a.new_empty((M, N), dtype=out_dtype)
+            else:
+                with _allocating(stream):
+                    out = a.new_empty((M, N), dtype=out_dtype)
         elif out.shape != (M, N) or out.dtype not in (torch.bfloat16, torch.float32) or \
                 out.get_device() != a.get_device() or (N > 1 and out.stride(1) != 1):
             raise ValueError("matmul: out must be bf16 or fp32 [M, N] with contiguous rows, on the rows' device")
