@@ -391,15 +391,23 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
     // ------------------------------------------------- MMA issuer ---
     uint32_t i = 0;
     uint32_t c = 0, other = 0;   // blocks given to the set at hand and to the other one
+    uint32_t phase = 0;
     int s = 0, set = 0;
-    bool ok = true;
+    bool ready = false;          // a test of a block's barriers takes some 85 cycles: made behind the block before it
     while (w.more()) {
       const uint32_t b = set * DBS + c % DBS;
       const uint32_t idesc = make_idesc_e4m3(128, (w.d.nr + 15) & ~15);
-      ok = ab.wait(&d_empty[b], ((c / DBS) & 1) ^ 1, kTagDEmpty, i, w.u) &&
-           ab.wait(&full[s], (i / NST) & 1, kTagWFull, i, w.u);
-      if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+      if (!__all_sync(0xFFFFFFFFu, ready)) {
+        const bool ok = ab.wait(&d_empty[b], ((c / DBS) & 1) ^ 1, kTagDEmpty, i, w.u) &&
+                        ab.wait(&full[s], phase, kTagWFull, i, w.u);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      }
       tc_fence_after();
+      const int s1 = s + 1 == NST ? 0 : s + 1;
+      const bool turn = Cfg::kSets == 2 && S == 1 && w.kb + 1 == w.k1;   // the next tile is the other set's
+      const uint32_t c1 = turn ? other : c + 1;
+      ready = mbar_test_wait(&d_empty[(turn ? set ^ 1 : set) * DBS + c1 % DBS], ((c1 / DBS) & 1) ^ 1);
+      ready &= mbar_test_wait(&full[s1], s1 == 0 ? phase ^ 1 : phase);
       if (elect_one()) {
         uint8_t* src = smem + s * Cfg::kStageBytes;
         const uint64_t rd = make_sdesc_sw128(smem_u32(src + NMAT * kFp8WBytes));
@@ -414,17 +422,15 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
         mma_commit(&d_full[b]);
       }
       __syncwarp();
-      if (++s == NST) s = 0;
+      if (s1 == 0) phase ^= 1;
+      s = s1;
       ++i;
-      ++c;
-      const int u = w.u;
-      w.next();
-      if (Cfg::kSets == 2 && S == 1 && w.u != u) {   // the next tile is the other set's
-        const uint32_t t = c;
-        c = other;
-        other = t;
+      if (turn) {
+        other = c + 1;
         set ^= 1;
       }
+      c = c1;
+      w.next();
     }
     if (i > 0) {   // drain: every MMA this warp issued has completed
       if (elect_one()) mma_commit(drain_bar);
@@ -447,7 +453,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
     uint32_t* tmax = tmax0 + set * 4 * BN;
     uint32_t i = 0, x_phase = 0;                         // i: blocks of this set so far
     if (set > 0 && turns == 1) w.u = w.units;            // nothing for this set
-    bool ok = true;
+    bool ok = true, ready = false;                       // ready: as of the MMA warp
     // Scales: lane j holds the weights' of block kb0 + j, 32 blocks at a time, and those of token row 32 q + j for
     // the next two blocks.  A tile's first ones are requested before the tile before it is finished.
     Fp8Unit d = {};
@@ -491,8 +497,11 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
         row_scales(kb + 2, sr2);
         __syncwarp();   // the row scales stand in shared memory
         const int b = set * DBS + i % DBS;
-        if (!(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[b], (i / DBS) & 1, kTagDFull, i, w.u)))) break;
+        if (!__all_sync(0xFFFFFFFFu, ready) &&
+            !(ok = __all_sync(0xFFFFFFFFu, ab.wait(&d_full[b], (i / DBS) & 1, kTagDFull, i, w.u))))
+          break;
         tc_fence_after();
+        ready = mbar_test_wait(&d_full[set * DBS + (i + 1) % DBS], ((i + 1) / DBS) & 1);
         unsigned long long ws[NMAT];
 #pragma unroll
         for (int m = 0; m < NMAT; ++m) {
