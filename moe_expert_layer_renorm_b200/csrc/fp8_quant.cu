@@ -20,7 +20,7 @@ constexpr int kFp8Block = 128;
 constexpr float kFp8Max = 448.0f;
 constexpr float kFp8Floor = 0x1p-100f;
 
-static inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+static inline int fp8_blocks(int n) { return int((unsigned(n) + kFp8Block - 1) / kFp8Block); }
 
 // The block's factors: code = e4m3((x * mul) / div).
 struct Fp8Scale {
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(256) fp8_quant_rows_kernel(const T* __restrict
                                                              uint8_t* __restrict__ codes, long long ld_codes,
                                                              float* __restrict__ scales, long long ld_scales) {
   pdl_enter();
-  const uint32_t nb = (K + kFp8Block - 1) / kFp8Block, groups = uint32_t(M) * nb;   // < 2^31
+  const uint32_t nb = (uint32_t(K) + kFp8Block - 1) / kFp8Block, groups = uint32_t(M) * nb;   // < 2^31
   const uint32_t stride = gridDim.x * 32u;
   const int sub = threadIdx.x & 7;
   Raw16<T> raw;

@@ -148,3 +148,11 @@ def test_ffn_refuses_more_blocks_than_32_bits_count(L):
         assert _lib.ffn_fp8_workspace_size(T, H, 256, 8, 1) == 0
         assert _lib.ffn_fp8_workspace_size(T, 256, H, 8, 1) == 0
     assert _lib.ffn_fp8_workspace_size((1 << 22) - 1, H, 256, 8, 1) > 0
+
+
+def test_sizes_at_the_end_of_int(L):
+    big = (1 << 31) - 1
+    assert quant(L, K=big, ld=big, ldc=1 << 31, lds=1 << 23) == INVALID      # fewer scales than blocks
+    assert quant(L, M=128, K=big, ld=big, ldc=1 << 31, lds=1 << 24) == INVALID   # 2^31 blocks
+    assert L.ft_fp8_pack(A, big, 128, A, 128, A, 1, None) == INVALID
+    assert L.ft_fp8_pack(A, 128, big, A, 1 << 31, A, 1 << 23, None) == INVALID
