@@ -88,32 +88,32 @@ __device__ __forceinline__ float inverse_sum(float z) { return z == 0.0f ? 0.0f 
 
 constexpr int kBalCluster = 8;   // CTAs that add up their sums through distributed shared memory
 
-// Sums over the tokens, in clusters of eight CTAs: a CTA's warps add up their
+// Sums over the tokens, in clusters of eight CTAs of W warps: a CTA's warps add up their
 // tokens' probabilities in registers, the CTA its warps', and CTA r of a
 // cluster the eight CTAs' sums of its eighth of the experts.  All additions
 // have a fixed order.  One cluster alone (a small batch) finishes counts and
 // loss itself; more of them leave part_p, part_c [clusters][E] and part_n
 // [clusters] to balance_finish_kernel.  A token's logits are requested behind
 // the token before it.
-template <int V, int NV>
-__global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(kBalThreads)
+template <int V, int NV, int W>
+__global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(32 * W)
 balance_kernel(const float* __restrict__ logits, long long ld, const int32_t* __restrict__ ids,
                const uint8_t* __restrict__ valid, int T, int E, int k, float coef, float* __restrict__ part_p,
                int32_t* __restrict__ part_c, int32_t* __restrict__ part_n, int32_t* __restrict__ counts,
                int32_t* __restrict__ n_valid, float* __restrict__ loss) {
   pdl_enter();
   extern __shared__ float bal_smem[];
-  float* sums = bal_smem;                                          // [kBalWarps][E], then [0] the CTA's
-  int* cnt = reinterpret_cast<int*>(bal_smem + kBalWarps * E);     // [E], then the valid tokens
-  float* terms = reinterpret_cast<float*>(cnt + E + 1);            // [kBalWarps]
-  float* cta_term = terms + kBalWarps;                             // [1]
+  float* sums = bal_smem;                                          // [W][E], then [0] the CTA's
+  int* cnt = reinterpret_cast<int*>(bal_smem + W * E);     // [E], then the valid tokens
+  float* terms = reinterpret_cast<float*>(cnt + E + 1);            // [W]
+  float* cta_term = terms + W;                             // [1]
   for (int e = threadIdx.x; e <= E; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int step = gridDim.x * kBalWarps;
+  const int step = gridDim.x * W;
   float acc[NV * V] = {};
   int n = 0;
-  int t = blockIdx.x * kBalWarps + warp;
+  int t = blockIdx.x * W + warp;
   float next[NV * V];
   bool live = t < T && (!valid || __ldg(valid + t));
   if (live) load_logits<V, NV>(logits + t * ld, E, lane, next);
@@ -145,7 +145,7 @@ balance_kernel(const float* __restrict__ logits, long long ld, const int32_t* __
   for (int e = threadIdx.x; e < E; e += blockDim.x) {
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kBalWarps; ++w) s += sums[w * E + e];
+    for (int w = 0; w < W; ++w) s += sums[w * E + e];
     sums[e] = s;
   }
   cluster_sync();
@@ -186,7 +186,7 @@ balance_kernel(const float* __restrict__ logits, long long ld, const int32_t* __
   __syncthreads();
   if (threadIdx.x == 0) {
     float s = 0.0f;
-    for (int w = 0; w < kBalWarps; ++w) s += terms[w];
+    for (int w = 0; w < W; ++w) s += terms[w];
     *cta_term = s;
   }
   cluster_sync();
@@ -359,13 +359,16 @@ static cudaError_t balance_variant(int E, bool vec, F f) {
   return f(integral_constant<int, 1>(), integral_constant<int, 32>());
 }
 
-// Clusters for T tokens: one, which needs no second launch, up to four tokens a
-// warp (T = 256), else enough for a CTA a SM: more of them cost more in sums
-// than they hide (8192 x 512, loss and gradient: 21.3 us, with two a SM 22.0,
-// with four 25.3).
+// Clusters for T tokens: one of 8 warps a CTA, which needs no second launch, up
+// to four tokens a warp (T = 256), else enough for a CTA of 16 warps a SM.  More
+// of them cost more in sums than they hide, fewer warps hide less (8192 x 512,
+// loss and gradient: 20.1 us; with 8 warps 21.3, and two CTAs a SM 22.0, four
+// 25.3; 64 x 128 in CTAs of 16 warps: 6.5 us instead of 6.2).
+constexpr int kBalManyWarps = 16;
 static int balance_clusters(int T, int num_sms) {
   if (T <= 4 * kBalWarps * kBalCluster) return 1;
-  return std::max(1, std::min((T + kBalWarps * kBalCluster - 1) / (kBalWarps * kBalCluster), num_sms / kBalCluster));
+  constexpr int per = kBalManyWarps * kBalCluster;
+  return std::max(2, std::min((T + per - 1) / per, num_sms / kBalCluster));
 }
 static size_t balance_ws_bytes(int T, int E, int num_sms) {
   return size_t(balance_clusters(T, num_sms)) * (2 * size_t(E) + 1) * 4;
@@ -380,10 +383,18 @@ static cudaError_t launch_balance(const float* logits, long long ld, const int32
   int32_t* part_n = part_c + size_t(clusters) * E;
   const bool vec = E % 4 == 0 && ld % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0;
   const cudaError_t e = balance_variant(E, vec, [&](auto v, auto nv) {
+    constexpr int V = decltype(v)::value, NV = decltype(nv)::value;
+    const bool one = clusters == 1;
+    const int warps = one ? kBalWarps : kBalManyWarps;
+    const size_t smem = ((warps + 1) * size_t(E) + warps + 4) * 4;
+    auto kern = one ? balance_kernel<V, NV, kBalWarps> : balance_kernel<V, NV, kBalManyWarps>;
+    if (smem > 48 * 1024) {
+      const cudaError_t a = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+      if (a != cudaSuccess) return a;
+    }
     ProfileScope prof(FT_KERNEL_BALANCE, s);
-    return launch_pdl(balance_kernel<decltype(v)::value, decltype(nv)::value>, dim3(clusters * kBalCluster),
-                      dim3(kBalThreads), ((kBalWarps + 1) * size_t(E) + kBalWarps + 4) * 4, s, logits, ld, ids, valid, T,
-                      E, k, coef, part_p, part_c, part_n, counts, n_valid, loss);
+    return launch_pdl(kern, dim3(clusters * kBalCluster), dim3(32 * warps), smem, s, logits, ld, ids, valid, T, E, k,
+                      coef, part_p, part_c, part_n, counts, n_valid, loss);
   });
   if (e != cudaSuccess || clusters == 1) return e;
   ProfileScope prof(FT_KERNEL_BALANCE, s);
