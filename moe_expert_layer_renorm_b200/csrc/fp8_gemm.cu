@@ -53,6 +53,7 @@ struct Fp8Params {
   int E, num_slots;
   int split;                  // CTAs (one cluster) that share a tile's K blocks
   int early;                  // weights and groups are older than the kernel before this one
+  int share;                  // host: the kernels that share a SM
 };
 
 struct Fp8Unit {
@@ -115,19 +116,23 @@ __device__ __forceinline__ uint32_t abs_bits(float v) {
 
 // ---------------------------------------------------------- few rows ---
 
-template <int NMAT, int BN>
+// SHARE: gate/up and down leave each other room on a SM, so that the down
+// kernel's first weights are on their way while gate/up still runs (one set of
+// epilogue warps, 3 or 4 stages, 256 columns of tensor memory).
+template <int NMAT, int BN, bool SHARE>
 struct Fp8StreamCfg {
   // Two sets of four epilogue warps take turns at the tiles where registers allow: a down tile of 6 blocks is finished
   // in some 7000 cycles, longer than its weights take to arrive.
-  static constexpr int kSets = NMAT * BN <= 64 ? 2 : 1;
+  static constexpr int kSets = NMAT * BN <= 64 && !SHARE ? 2 : 1;
   static constexpr int kThreads = 64 + 128 * kSets;             // TMA warp, MMA warp, epilogue warps
   static constexpr int kStageBytes = NMAT * kFp8WBytes + BN * 128;
   // partial sums from the other CTAs of the cluster; none where they would take more than 32 KB
   static constexpr int kXBytes = NMAT * BN * 512 <= 32768 ? NMAT * BN * 512 : 0;
-  static constexpr int kStages = (208 * 1024 - kXBytes) / kStageBytes;
+  static constexpr int kStages = SHARE ? (NMAT == 2 ? 4 : 3) : (208 * 1024 - kXBytes) / kStageBytes;
   // accumulator buffers, as many as tensor memory holds up to 16: the MMAs, and with them the stream of weights,
   // run on while the epilogue finishes a tile (4400 cycles) and meets the next one's scales (3500, from HBM)
-  static constexpr int kDB = 512 / (NMAT * BN) < 16 ? 512 / (NMAT * BN) : 16;
+  static constexpr int kCols = SHARE ? 256 : 512;
+  static constexpr int kDB = kCols / (NMAT * BN) < 16 ? kCols / (NMAT * BN) : 16;
   static constexpr int kTmemCols = kDB * NMAT * BN;    // a power of two, 256 or 512
   static constexpr int kBars = (2 * kStages + 2 * kDB + 3 + kSets + 1) / 2 * 2;   // even: what follows is 16-byte aligned
   static constexpr int kFixedBytes = 1024 + kStages * kStageBytes + kXBytes + kBars * 8 + kSets * 8 * BN * 4 + 64;
@@ -299,11 +304,11 @@ __device__ __forceinline__ bool fp8_exchange(float (&acc)[NMAT][BN], float* xbuf
 // A tile's weights stand in memory longer than its token rows (`early`: the
 // kernel before this one makes those rows): the first ring of weights is
 // requested before that kernel has ended.
-template <int NMAT, int BN>
-__global__ void __launch_bounds__(Fp8StreamCfg<NMAT, BN>::kThreads, 1)
+template <int NMAT, int BN, bool SHARE>
+__global__ void __launch_bounds__(Fp8StreamCfg<NMAT, BN, SHARE>::kThreads, SHARE ? 2 : 1)
 fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
                   const __grid_constant__ CUtensorMap tm_w1, const __grid_constant__ CUtensorMap tm_rows) {
-  using Cfg = Fp8StreamCfg<NMAT, BN>;
+  using Cfg = Fp8StreamCfg<NMAT, BN, SHARE>;
   constexpr int NST = Cfg::kStages, DB = Cfg::kDB, DBS = DB / Cfg::kSets;   // DBS: accumulator buffers of one set
   extern __shared__ uint8_t smem_raw[];
   __shared__ int warp_sums[32];
@@ -1266,12 +1271,12 @@ static int fp8_cluster_ctas(K kern, int threads, int smem, int cluster, int num_
 // time on the busiest cluster, counted in K blocks: tiles a cluster takes x
 // blocks a CTA, three more a split tile for its exchange (some 2.5 us against
 // 0.75 us a block of gate/up).
-template <int NMAT, int BN>
+template <int NMAT, int BN, bool SHARE>
 static cudaError_t launch_fp8_stream(Fp8Params p, double units, long long most, int num_sms, const CUtensorMap& w0,
                                      const CUtensorMap& w1, const CUtensorMap& rows, cudaStream_t s) {
-  using Cfg = Fp8StreamCfg<NMAT, BN>;
+  using Cfg = Fp8StreamCfg<NMAT, BN, SHARE>;
   static std::atomic<int> allowed[64], ctas[64][4];   // by device
-  auto kern = fp8_stream_kernel<NMAT, BN>;
+  auto kern = fp8_stream_kernel<NMAT, BN, SHARE>;
   constexpr int kMost = Cfg::smem_bytes(1024);
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1279,6 +1284,8 @@ static cudaError_t launch_fp8_stream(Fp8Params p, double units, long long most, 
   dev &= 63;
   if (!allowed[dev].load()) {
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e == cudaSuccess && SHARE)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     allowed[dev].store(1);
   }
@@ -1323,9 +1330,11 @@ static cudaError_t launch_fp8_any(int bn, Fp8Params p, long long out_rows, doubl
   CUtensorMap out = rows;
   const bool mapped = bn < 128 || NMAT == 2 || make_fp8_out_map(p.out, p.out_type, out_rows, p.N, p.ldo, &out);
   switch (bn) {
-    case 16: return launch_fp8_stream<NMAT, 16>(p, units, most, num_sms, w0, w1, rows, s);
-    case 32: return launch_fp8_stream<NMAT, 32>(p, units, most, num_sms, w0, w1, rows, s);
-    case 64: return launch_fp8_stream<NMAT, 64>(p, units, most, num_sms, w0, w1, rows, s);
+    case 16:
+      return p.share ? launch_fp8_stream<NMAT, 16, true>(p, units, most, num_sms, w0, w1, rows, s)
+                     : launch_fp8_stream<NMAT, 16, false>(p, units, most, num_sms, w0, w1, rows, s);
+    case 32: return launch_fp8_stream<NMAT, 32, false>(p, units, most, num_sms, w0, w1, rows, s);
+    case 64: return launch_fp8_stream<NMAT, 64, false>(p, units, most, num_sms, w0, w1, rows, s);
     case 128:   // experts: H is a multiple of 64, every output has a map
       return mapped ? launch_fp8_tile<NMAT, false, true>(p, most, num_sms, w0, w1, rows, out, s) : cudaErrorInvalidValue;
     default:
@@ -1521,6 +1530,7 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
     p.E = E;
     p.num_slots = L.num_slots;
     p.early = 1;
+    p.share = pl.bn == 16 && pl.tiles * pl.mt1 <= device_sm_count();
   } else {
     p.units = units1;
     p.num_units = counts;
