@@ -409,6 +409,7 @@ static cudaError_t launch_route_backward(const float* logits, long long ld, cons
                                          float* dlogits, long long ldd, int num_sms, cudaStream_t s) {
   const bool vec = E % 4 == 0 && ld % 4 == 0 && ldd % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0;
+  // four CTAs a SM, as many as fit (8192 x 512, loss and gradient: 20.0 us, with two 22.6, with eight in turns 20.9)
   const int blocks = int(std::min<long long>((T + kBalWarps - 1) / kBalWarps, 4LL * num_sms));
   return balance_variant(E, vec, [&](auto v, auto nv) {
     ProfileScope prof(FT_KERNEL_ROUTE_BACKWARD, s);
