@@ -337,6 +337,52 @@ def test_ffn_bad_token_reads_as_zeros(rows):
     f.check(out)
 
 
+def test_ffn_bad_token_of_rows_copied_from_their_tokens():
+    f = Ffn([200, 130, 190], 320, 512, 2, seed=4)      # many rows, two a token
+    good = f.perm.copy()
+    f.perm[1], f.perm[2] = 2 * f.T, -1
+    out = f.run()
+    assert _status() == _lib.FT_DEV_BAD_INDEX
+    assert (out[1:3] == 0).all()
+    f.perm[:] = good
+    kept = torch.ones(len(good), dtype=torch.bool)
+    kept[1:3] = False
+    again = f.run()
+    assert torch.equal(out[kept], again[kept])
+    f.check(again)
+
+
+@pytest.mark.parametrize("rows,H,I,k", [([1] * 8, 2048, 768, 8), ([3, 0, 2, 4], 512, 320, 3), ([140, 90, 130], 256, 512, 2)])
+def test_ffn_calls_at_once_on_three_streams_and_in_graphs(rows, H, I, k):
+    fs = [Ffn(rows, H, I, k, seed=30 + i) for i in range(3)]
+    want = [f.run().clone() for f in fs]
+    tables = [torch.from_numpy(f.table).cuda() for f in fs]
+    streams = [torch.cuda.Stream() for _ in fs]
+    torch.cuda.synchronize()
+    for f in fs:
+        f.layer.out_perm.fill_(-5.0)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for f, t, s in zip(fs, tables, streams):
+            f.layer.ffn(f.x, t, f.pool, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(f.layer.out_perm, w) for f, w in zip(fs, want))
+    graphs = []
+    for f, t in zip(fs, tables):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(4):
+                f.layer.ffn(f.x, t, f.pool)
+        f.layer.out_perm.fill_(-5.0)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(f.layer.out_perm, w) for f, w in zip(fs, want))
+
+
 @pytest.mark.parametrize("rows", [[5, 4], [200, 130]])
 def test_ffn_non_finite_tokens_stay_in_their_rows(rows):
     f = Ffn(rows, 256, 512, 1, seed=4)
