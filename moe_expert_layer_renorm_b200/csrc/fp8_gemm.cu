@@ -596,7 +596,7 @@ fp8_stream_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
           if (j >= nc) break;
           const uint32_t m = max(max(tmax[j], tmax[BN + j]), max(tmax[2 * BN + j], tmax[3 * BN + j]));
           const Fp8Scale f = fp8_scale_of(__uint_as_float(m));
-          if (feat < p.N) h[(rb0 + j) * p.ldo + feat] = uint8_t(cvt_e4m3x2(acc[0][j] * fp8_factor_of(f), 0.0f));
+          if (feat < p.N) h[(rb0 + j) * p.ldo + feat] = uint8_t(fp8_codes2(acc[0][j], 0.0f, f));
           if (row == 0) p.hs[(rb0 + j) * hb + done.ft] = f.scale;
         }
         if (!(ok = epi.sync(lane))) break;   // the maxima are read before the next tile's are written
@@ -1072,7 +1072,6 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
         if (!(ok = epi.sync(lane))) break;
         m = max(m, tmax[parity * 256 + (half ^ 1) * 128 + row]);
         const Fp8Scale f = fp8_scale_of(__uint_as_float(m));
-        const float inv = fp8_factor_of(f);
         const int f0 = ft * 128 + half * 64;
         if (live) {
           if (half == 0) p.hs[(long long)(rb + row) * ((p.N + kFp8Block - 1) / kFp8Block) + ft] = f.scale;
@@ -1083,8 +1082,7 @@ fp8_tile_kernel(const Fp8Params p, const __grid_constant__ CUtensorMap tm_w0,
               uint32_t o[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                o[q] = cvt_e4m3x2(h[16 * c + 4 * q] * inv, h[16 * c + 4 * q + 1] * inv) |
-                       (cvt_e4m3x2(h[16 * c + 4 * q + 2] * inv, h[16 * c + 4 * q + 3] * inv) << 16);
+                o[q] = fp8_codes4(h[16 * c + 4 * q], h[16 * c + 4 * q + 1], h[16 * c + 4 * q + 2], h[16 * c + 4 * q + 3], f);
               dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
             }
           }

@@ -48,10 +48,6 @@ __device__ __forceinline__ Fp8Scale fp8_scale_of(float amax) {
   if (inf) f.div = 1.0f;
   return f;
 }
-// For values that fp32 arithmetic has just computed (h) one product with
-// 448 / m does: no tie of theirs is meant, and a quotient within
-// 2^-23 of one may go either way.
-__device__ __forceinline__ float fp8_factor_of(const Fp8Scale& f) { return __fmul_rn(f.mul, f.rcp); }
 // Two values -> two E4M3 codes, the first in the low byte (nearest even,
 // saturating at 448; NaN -> 0x7F).
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
