@@ -101,12 +101,20 @@ __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&v)
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[32]) { tmem_ld_32x32b_x32(taddr, v); }
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[16]) { tmem_ld_32x32b_x16(taddr, v); }
 
-// silu(g) u with the hardware exponential and a fast divide: a few fp32 steps
-// (as the exponential overflows the quotient goes to 0, its limit).  One h a
-// thread and column stands between a tile's last block and the next tile's
-// first: with expf and an IEEE division here the gate/up kernel of 4096 skewed
-// tokens (2048 x 768, 128 experts, k = 8) takes 197 us instead of 149.
-__device__ __forceinline__ float fp8_silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
+// silu(g) u, as g s u with s = (g >= 0 ? 1 : e) / (1 + e) and e = e^-|g|: nothing
+// overflows, whatever g, and the divisor lies in [1, 2], so that an approximate
+// reciprocal and one remainder step (as quotient_by) give the quotient to a step
+// or two of fp32.  A non-finite g follows g / (1 + e^-g): e is 0 or NaN.
+// One h a thread and column stands between a tile's last block and the next
+// tile's first.  The hardware exponential and a fast divide would save 5 us of
+// 278 of the FFN (4096 skewed tokens, 2048 x 768, 128 experts, k = 8), but lose up
+// to 2^-18 of h, and all of it where 1 + e^-g passes 2^126.
+__device__ __forceinline__ float fp8_silu_mul(float g, float u) {
+  const float e = expf(-fabsf(g)), d = 1.0f + e;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return g * quotient_by(g >= 0.0f ? 1.0f : e, d, r) * u;
+}
 
 // |v| for a maximum that leaves NaN out, as ordered bits.
 __device__ __forceinline__ uint32_t abs_bits(float v) {

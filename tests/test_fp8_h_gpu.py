@@ -65,3 +65,29 @@ def test_ties_of_h_go_to_the_even_code(js, T):
     assert ties >= 12
     out = _one_expert(x, gate, up)
     assert np.array_equal(out, np.broadcast_to(want, out.shape))
+
+
+@pytest.mark.parametrize("at_once", [11, 22, 60, 66])
+def test_silu_to_a_few_fp32_steps(at_once):
+    """One h alone in each block of 128 is the block's largest, and the output 448 h.
+
+    G and U are exact.  In units of 2^-24: the exponential 4 (two steps), 1 + e one, the quotient two, its product with
+    G one (with U, a power of two, none), the scale one, the output one: 10, and 12 with the products of these.  Where
+    e^-|G| is subnormal it is held to 2^-149."""
+    U = 2.0 ** 30
+    x0 = np.array([s * m / 8 * 2.0 ** e for e in range(-3, 1) for m in range(8, 16) for s in (1, -1)] + [2.0, -2.0])
+    x = torch.zeros(len(x0), H)
+    x[:, 0], x[:, 1], x[:, 101] = torch.from_numpy(x0), 1.0, 448.0
+    gate, up = torch.zeros(I, H), torch.zeros(I, H)
+    wg = np.array([4.0, 44.0])
+    for b in range(2):
+        gate[b * 128, 0], up[b * 128, 1] = wg[b], U
+        gate[b * 128, 100], up[b * 128, 100] = 448.0, 448.0 * U
+    out = np.concatenate([_one_expert(x[i:i + at_once], gate, up) for i in range(0, len(x0), at_once)])
+    G = x0[:, None] * wg
+    h = G * U / (1 + np.exp(-G))
+    got = out[:, [0, 128]] / 448
+    assert np.all(np.abs(got - h) <= 12 * 2.0 ** -24 * np.abs(h) + np.abs(G) * U * 2.0 ** -149)
+    rest = np.ones(H, bool)
+    rest[[0, 128]] = False
+    assert not out[:, rest].any()
