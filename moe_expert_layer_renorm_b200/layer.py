@@ -204,6 +204,7 @@ class MoELayer:
 
     def layer(self, x: torch.Tensor, logits: torch.Tensor, slot_table: torch.Tensor, pool: ExpertPool,
               stream=None) -> None:
+        assert self.out_perm.dtype == torch.float32, "bf16 expert outputs are for FP8 pools"
         _lib.layer_nvfp4(x.data_ptr(), logits.data_ptr(), self.T, self.H, self.I, self.E, self.k, self.mode,
                          slot_table.data_ptr(), pool.ptr, pool.layout, self.ids.data_ptr(), self.w.data_ptr(),
                          self.offsets.data_ptr(), self.perm_src.data_ptr(), self.pair_to_row.data_ptr(),
