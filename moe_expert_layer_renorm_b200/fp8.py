@@ -9,13 +9,12 @@ allocated on that stream.
 """
 from __future__ import annotations
 
-import contextlib
 from typing import Optional, Tuple
 
 import torch
 
 from . import _lib
-from .layer import _stream
+from .layer import _allocating, _stream
 
 FP8 = torch.float8_e4m3fn
 _TYPES = {torch.float32: _lib.FT_F32, torch.bfloat16: _lib.FT_BF16, torch.float16: _lib.FT_F16}
@@ -28,11 +27,6 @@ def _blocks(n: int) -> int:
 def _here(t: torch.Tensor) -> None:
     if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {t.device}, which is not the current device")
-
-
-def _allocating(stream):
-    """New tensors belong to `stream`: one of the current stream's could still be in use there."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def empty_codes(rows: int, K: int, device) -> torch.Tensor:

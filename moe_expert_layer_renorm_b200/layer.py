@@ -6,6 +6,7 @@ memory with torch and forwards pointers (there is no fallback path).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
@@ -24,6 +25,11 @@ def _stream(s: Optional[torch.cuda.Stream]) -> int:
     """The handle of s, or of the current device's current stream (without the Stream object that
     torch.cuda.current_stream() makes of it, some 5 us a call)."""
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if s is None else s.cuda_stream
+
+
+def _allocating(stream):
+    """New tensors belong to `stream`: one of the current stream's could still be in use there."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def untile(block: np.ndarray, N: int, width: int, row_bytes: int) -> np.ndarray:
@@ -145,31 +151,22 @@ class MoELayer:
         self.fp8_ws_bytes = _lib.ffn_fp8_workspace_size(T, H, I, E, k)
         self._perm_ws = self._ffn_ws = self._layer_ws = self._fp8_ws = None
 
-    # workspaces, allocated on first use: the separate calls' (permute, ffn) and
-    # the whole-layer call's, which is zero-filled once and left ready by every call
-    @property
-    def perm_ws(self) -> torch.Tensor:
-        if self._perm_ws is None:
-            self._perm_ws = torch.empty(max(self.perm_ws_bytes, 256), dtype=torch.uint8, device=self.dev)
-        return self._perm_ws
+    # workspaces, allocated on first use, on the stream of that call: the separate calls'
+    # (permute, ffn) and the whole-layer call's, which is zero-filled once and left ready
+    # by every call
+    def _workspace(self, name: str, stream=None) -> torch.Tensor:
+        ws = getattr(self, "_" + name)
+        if ws is None:
+            make = torch.zeros if name == "layer_ws" else torch.empty
+            with _allocating(stream):
+                ws = make(max(getattr(self, name + "_bytes"), 256), dtype=torch.uint8, device=self.dev)
+            setattr(self, "_" + name, ws)
+        return ws
 
-    @property
-    def ffn_ws(self) -> torch.Tensor:
-        if self._ffn_ws is None:
-            self._ffn_ws = torch.empty(max(self.ffn_ws_bytes, 256), dtype=torch.uint8, device=self.dev)
-        return self._ffn_ws
-
-    @property
-    def fp8_ws(self) -> torch.Tensor:
-        if self._fp8_ws is None:
-            self._fp8_ws = torch.empty(max(self.fp8_ws_bytes, 256), dtype=torch.uint8, device=self.dev)
-        return self._fp8_ws
-
-    @property
-    def layer_ws(self) -> torch.Tensor:
-        if self._layer_ws is None:
-            self._layer_ws = torch.zeros(max(self.layer_ws_bytes, 256), dtype=torch.uint8, device=self.dev)
-        return self._layer_ws
+    perm_ws = property(lambda self: self._workspace("perm_ws"))
+    ffn_ws = property(lambda self: self._workspace("ffn_ws"))
+    fp8_ws = property(lambda self: self._workspace("fp8_ws"))
+    layer_ws = property(lambda self: self._workspace("layer_ws"))
 
     def route(self, logits: torch.Tensor, stream=None) -> None:
         _lib.route(logits.data_ptr(), self.T, self.E, self.k, self.mode, self.ids.data_ptr(), self.w.data_ptr(),
@@ -177,12 +174,14 @@ class MoELayer:
 
     def permute(self, stream=None) -> None:
         _lib.permute(self.ids.data_ptr(), self.T, self.k, self.E, self.offsets.data_ptr(), self.perm_src.data_ptr(),
-                     self.pair_to_row.data_ptr(), self.perm_ws.data_ptr(), self.perm_ws_bytes, _stream(stream))
+                     self.pair_to_row.data_ptr(), self._workspace("perm_ws", stream).data_ptr(), self.perm_ws_bytes,
+                     _stream(stream))
 
     def route_permute(self, logits: torch.Tensor, stream=None) -> None:
         _lib.route_permute(logits.data_ptr(), self.T, self.E, self.k, self.mode, self.ids.data_ptr(),
                            self.w.data_ptr(), self.offsets.data_ptr(), self.perm_src.data_ptr(),
-                           self.pair_to_row.data_ptr(), self.perm_ws.data_ptr(), self.perm_ws_bytes, _stream(stream))
+                           self.pair_to_row.data_ptr(), self._workspace("perm_ws", stream).data_ptr(),
+                           self.perm_ws_bytes, _stream(stream))
 
     def ffn(self, x: torch.Tensor, slot_table: torch.Tensor, pool: ExpertPool, stream=None) -> None:
         if pool.fmt == _lib.FT_SCALE_FP8:
@@ -190,12 +189,13 @@ class MoELayer:
                          self.offsets.data_ptr(), slot_table.data_ptr(), pool.ptr, pool.layout,
                          self.out_perm.data_ptr(),
                          _lib.FT_F32 if self.out_perm.dtype == torch.float32 else _lib.FT_BF16,
-                         self.fp8_ws.data_ptr(), self.fp8_ws_bytes, _stream(stream))
+                         self._workspace("fp8_ws", stream).data_ptr(), self.fp8_ws_bytes, _stream(stream))
             return
         assert self.out_perm.dtype == torch.float32, "bf16 expert outputs are for FP8 pools"
         _lib.ffn_nvfp4(x.data_ptr(), self.T, self.H, self.I, self.E, self.k, self.perm_src.data_ptr(),
                        self.offsets.data_ptr(), slot_table.data_ptr(), pool.ptr, pool.layout,
-                       self.out_perm.data_ptr(), self.ffn_ws.data_ptr(), self.ffn_ws_bytes, _stream(stream))
+                       self.out_perm.data_ptr(), self._workspace("ffn_ws", stream).data_ptr(), self.ffn_ws_bytes,
+                       _stream(stream))
 
     def combine(self, stream=None) -> None:
         combine = _lib.combine if self.out_perm.dtype == torch.float32 else _lib.combine_bf16
@@ -208,8 +208,8 @@ class MoELayer:
         _lib.layer_nvfp4(x.data_ptr(), logits.data_ptr(), self.T, self.H, self.I, self.E, self.k, self.mode,
                          slot_table.data_ptr(), pool.ptr, pool.layout, self.ids.data_ptr(), self.w.data_ptr(),
                          self.offsets.data_ptr(), self.perm_src.data_ptr(), self.pair_to_row.data_ptr(),
-                         self.out_perm.data_ptr(), self.y.data_ptr(), self.layer_ws.data_ptr(), self.layer_ws_bytes,
-                         _stream(stream))
+                         self.out_perm.data_ptr(), self.y.data_ptr(), self._workspace("layer_ws", stream).data_ptr(),
+                         self.layer_ws_bytes, _stream(stream))
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, slot_table: torch.Tensor, pool: ExpertPool,
                 stream=None) -> torch.Tensor:
