@@ -72,8 +72,9 @@ __device__ __forceinline__ void put_row(float* row, int E, int lane, const float
 
 // e^(logit - largest logit) in place of the logits (0 past E), and 1 / their
 // sum.  A row whose logits are all -inf has no probabilities: zeros and 0.
-// The hardware exponential: 2^-22 of a probability near 1, some 2^-20 of one
-// at e^-10, against the 2^-18 that the sums over thousands of tokens keep.
+// expf, as the router: a gradient takes its own p, and the hardware exponential
+// would lose 2^-18 of one at e^-80 (8192 x 512, loss and gradient: 21.8 us, with
+// it 19.8).
 template <int N>
 __device__ __forceinline__ void row_exps(float (&v)[N]) {
   float m = v[0];
@@ -82,7 +83,7 @@ __device__ __forceinline__ void row_exps(float (&v)[N]) {
   m = warp_max(m);
   if (m == -INFINITY) m = 0.0f;      // all -inf: exp gives zeros
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __expf(v[i] - m);
+  for (int i = 0; i < N; ++i) v[i] = expf(v[i] - m);
 }
 __device__ __forceinline__ float inverse_sum(float z) { return z == 0.0f ? 0.0f : 1.0f / z; }
 
