@@ -129,8 +129,10 @@ class ExpertParallelMoE:
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor, slot_table: torch.Tensor, pool: ExpertPool,
                 stream=None) -> torch.Tensor:
-        """The layer for this rank's T tokens; returns y fp32 [T, H]."""
+        """The layer for this rank's T tokens; returns y fp32 [T, H].  pool holds NVFP4 or MXFP4 experts."""
         L, k, H = self.layer, self.k, self.H
+        # before the first collective: a rank that received no rows would not notice, and wait for those that did
+        assert pool.fmt != _lib.FT_SCALE_FP8, "expert parallelism takes NVFP4 and MXFP4 pools"
         assert x.dtype == torch.bfloat16 and x.shape == (self.T, H) and x.is_contiguous()
         assert logits.dtype == torch.float32 and logits.shape == (self.T, self.E) and logits.is_contiguous()
         assert slot_table.dtype == torch.int32 and slot_table.numel() == self.E_local
