@@ -126,7 +126,7 @@ __device__ __forceinline__ uint32_t abs_bits(float v) {
 
 // SHARE: gate/up and down leave each other room on a SM, so that the down
 // kernel's first weights are on their way while gate/up still runs (one set of
-// epilogue warps, 3 or 4 stages, 256 columns of tensor memory).
+// epilogue warps, 3 or 4 stages, 8 accumulator buffers).
 template <int NMAT, int BN, bool SHARE>
 struct Fp8StreamCfg {
   // Two sets of four epilogue warps take turns at the tiles where registers allow: a down tile of 6 blocks is finished
@@ -139,7 +139,7 @@ struct Fp8StreamCfg {
   static constexpr int kStages = SHARE ? (NMAT == 2 ? 4 : 3) : (208 * 1024 - kXBytes) / kStageBytes;
   // accumulator buffers, as many as tensor memory holds up to 16: the MMAs, and with them the stream of weights,
   // run on while the epilogue finishes a tile (4400 cycles) and meets the next one's scales (3500, from HBM)
-  static constexpr int kCols = SHARE ? 256 : 512;
+  static constexpr int kCols = SHARE ? 128 * NMAT : 512;
   static constexpr int kDB = kCols / (NMAT * BN) < 16 ? kCols / (NMAT * BN) : 16;
   static constexpr int kTmemCols = kDB * NMAT * BN;    // a power of two, 256 or 512
   static constexpr int kBars = (2 * kStages + 2 * kDB + 3 + kSets + 1) / 2 * 2;   // even: what follows is 16-byte aligned
@@ -147,7 +147,20 @@ struct Fp8StreamCfg {
   static constexpr int smem_bytes(int E) { return kFixedBytes + 12 * (E + 1); }   // and the groups' table
   static_assert(kTmemCols >= 32 && kTmemCols <= 512 && (kTmemCols & (kTmemCols - 1)) == 0, "tensor memory");
   static_assert(smem_bytes(1024) <= 227 * 1024, "shared memory");
+  // CTAs that `left` bytes of a SM's shared memory hold (1 KB of each is the system's)
+  static constexpr int ctas_in(int left) { return left / (smem_bytes(1) + 1024); }
+  static constexpr int kSmLeft = 228 * 1024 - smem_bytes(1) - 1024;   // beside one CTA
 };
+// Whatever CTAs of the SHARE kernels shared memory lets on a SM, calls on other streams among them, tensor memory has
+// columns for: no CTA waits in the allocation, where the CTAs of two clusters could hold each other up without a limit.
+template <int BN>
+constexpr bool fp8_share_fits() {
+  using GateUp = Fp8StreamCfg<2, BN, true>;
+  using Down = Fp8StreamCfg<1, BN, true>;
+  return GateUp::ctas_in(228 * 1024) == 1 && Down::ctas_in(228 * 1024) * Down::kTmemCols <= 512 &&
+         GateUp::kTmemCols + Down::ctas_in(GateUp::kSmLeft) * Down::kTmemCols <= 512;
+}
+static_assert(fp8_share_fits<16>(), "tensor memory of the kernels that share a SM");
 
 
 // One lane of a converged warp.  The MMA warps run their loops as a whole warp
