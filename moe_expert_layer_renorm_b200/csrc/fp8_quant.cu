@@ -224,12 +224,13 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(const float* __restrict__
   __shared__ float warp_max[8];
   const int n = blockIdx.y * kFp8Block + (threadIdx.x >> 1);
   const int k0 = blockIdx.x * kFp8Block + (threadIdx.x & 1) * 64;
+  const int left = K - k0;   // values of the row from k0 on; k0 plus a place may pass 2^31
   const float* src = w + (long long)n * K + k0;
   float v[64];
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 64; ++i) {
-    v[i] = n < N && k0 + i < K ? __ldg(src + i) : 0.0f;
+    v[i] = n < N && i < left ? __ldg(src + i) : 0.0f;
     m = fmaxf(m, fabsf(v[i]));
   }
 #pragma unroll
@@ -240,20 +241,20 @@ __global__ void __launch_bounds__(256) fp8_pack_kernel(const float* __restrict__
   for (int i = 0; i < 8; ++i) m = fmaxf(m, warp_max[i]);
   const Fp8Scale f = fp8_scale_of(m);
   if (threadIdx.x == 0) scales[(long long)blockIdx.y * ld_scales + blockIdx.x] = f.scale;
-  if (blockIdx.x == 0 && int(gridDim.x + threadIdx.x) < ld_scales)
-    for (int c = gridDim.x + threadIdx.x; c < ld_scales; c += blockDim.x)
+  if (blockIdx.x == 0)
+    for (long long c = gridDim.x + threadIdx.x; c < ld_scales; c += blockDim.x)
       scales[(long long)blockIdx.y * ld_scales + c] = 0.0f;
   if (n >= N) return;
   uint8_t* dst = codes + (long long)n * ld_codes + k0;
 #pragma unroll
   for (int i = 0; i < 64; i += 4) {
     const uint32_t c = fp8_codes4(v[i], v[i + 1], v[i + 2], v[i + 3], f);
-    if (k0 + i + 4 <= K) {   // codes and ld_codes are multiples of 16
+    if (left - i >= 4) {   // codes and ld_codes are multiples of 16
       *reinterpret_cast<uint32_t*>(dst + i) = c;
     } else {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (k0 + i + j < K) dst[i + j] = uint8_t(c >> (8 * j));
+        if (i + j < left) dst[i + j] = uint8_t(c >> (8 * j));
     }
   }
 }
