@@ -5,6 +5,7 @@ import torch
 
 from moe_expert_layer_renorm_b200 import _lib
 from moe_expert_layer_renorm_b200.balance import RouterBalance
+from oracle import fp8 as F
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +58,33 @@ def test_loss_of_an_unlikely_choice(E):
     got = np.array([float(b.forward(l[i:i + 1], ids)) for i in range(len(D))])
     ref = float(np.float32(0.3)) * E * np.exp(-D) / (1 + np.exp(-D))
     assert np.all(np.abs(got - ref) <= 12 * U * ref)
+
+
+@pytest.mark.parametrize("T,E,k", [(8192, 512, 10), (5000, 1024, 8), (257, 100, 4), (256, 128, 8), (3000, 33, 2), (20000, 8, 2)])
+def test_loss_and_gradient_of_many_tokens(T, E, k):
+    """In U.  A probability: its argument |l - m|, the exponential 4, at most 32 places a lane and 5 exchanges in its
+    sum, the reciprocal and its product 2.  A sum over the tokens adds no more terms in a chain than a warp takes tokens
+    (all warps: 8 x 8 up to 256 tokens, else at least 8 x 16 of each of two clusters), then 16 warps, 8 CTAs and the
+    clusters, 18 on this device and 32 at most; the loss a product, one chain of at most 32 + 5 + 32 experts' terms and
+    6 for its factor.  All terms are positive."""
+    g = torch.Generator().manual_seed(T + E)
+    l = (torch.randn(T, E, generator=g) * 2.0 + torch.randn(E, generator=g)).cuda()
+    ids = l.topk(k, dim=-1).indices.int()
+    b = RouterBalance(T, E, k, 0.3)
+    loss = float(b.forward(l, ids))
+    d = b.backward(l, ids).double().cpu().numpy()
+    ln, coef = l.double().cpu().numpy(), float(np.float32(0.3))
+    counts, ref, dref = F.balance(ln, ids.cpu().numpy(), np.ones(T, bool), coef)
+    assert np.array_equal(b.counts.cpu().numpy(), counts)
+    spread = ln.max(1) - ln.min(1)
+    p_err = spread.max() + 4 + 32 + 5 + 2
+    tokens = T / (8 * 8 if T <= 256 else 2 * 8 * 16)
+    assert abs(loss - ref) <= 1.01 * (p_err + tokens + 1 + 16 + 8 + 32 + 1 + 32 + 5 + 32 + 6) * U * ref
+    # f p (c - mean): p and mean as above (the mean one product a place more), f six, the difference and products 4;
+    # the difference may cancel, so its errors are those of c + mean
+    p = np.exp(ln - ln.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    mean = (p * counts).sum(1, keepdims=True)
+    scale = coef * E / (float(T) ** 2 * k)
+    tol = 1.01 * U * scale * p * ((p_err + 10) * np.abs(counts - mean) + 4 * counts + (2 * p_err + 4) * mean)
+    assert np.all(np.abs(d - dref) <= tol)
