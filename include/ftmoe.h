@@ -392,7 +392,8 @@ FT_API int ft_mxfp4_pack(const float* w, int N, int K, uint8_t* codes, uint8_t* 
  * activations and 128 x 128 for weights.  Of a block with values x_i:
  *   m   = max(max |x_i|, 2^-100)           (NaN left out of the maximum)
  *   s   = m / 448                          (fp32, the stored scale)
- *   q_i = E4M3_rne_sat((448 x_i) / m)      (fp32 product, then fp32 division)
+ *   q_i = E4M3_rne_sat((448 x_i) / m)      (fp32 product, then its quotient, to a step of fp32 and
+ *                                           exact where fp32 holds it)
  * and the value of a code is e4m3(q_i) * s.  Ties go to the even code; for
  * bf16 and f16 inputs 448 x_i is exact, so the ties are those of the exact
  * quotient.  A NaN becomes the code 0x7F (NaN); an infinity makes the scale
@@ -438,7 +439,7 @@ FT_API int ft_fp8_gemm(const uint8_t* a, int64_t lda, const float* sa, int64_t l
  * t = perm_src[r] / k):
  *   (cx, sx)    = FP8 of x_t                       (as ft_fp8_quant_rows)
  *   G, U        = gate and up products of (cx, sx) (as ft_fp8_gemm, fp32)
- *   h           = G / (1 + e^-G) * U               (fp32)
+ *   h           = G / (1 + e^-G) * U               (to a few fp32 steps, also where e^-G overflows)
  *   (ch, sh)    = FP8 of h, per 128 of I
  *   out_perm[r] = down product of (ch, sh)         (fp32 sums, rounded once to out_type)
  * Arguments as for ft_moe_ffn_nvfp4, with an FP8 layout; out_perm is device

@@ -73,8 +73,8 @@ __device__ __forceinline__ void put_row(float* row, int E, int lane, const float
 // e^(logit - largest logit) in place of the logits (0 past E), and 1 / their
 // sum.  A row whose logits are all -inf has no probabilities: zeros and 0.
 // expf, as the router: a gradient takes its own p, and the hardware exponential
-// would lose 2^-18 of one at e^-80 (8192 x 512, loss and gradient: 21.8 us, with
-// it 19.8).
+// would lose 2^-18 of one at e^-80 (8192 x 512, loss and gradient: 22.3 us, with
+// it 20.6).
 template <int N>
 __device__ __forceinline__ void row_exps(float (&v)[N]) {
   float m = v[0];
@@ -363,8 +363,8 @@ static cudaError_t balance_variant(int E, bool vec, F f) {
 // Clusters for T tokens: one of 8 warps a CTA, which needs no second launch, up
 // to four tokens a warp (T = 256), else enough for a CTA of 16 warps a SM.  More
 // of them cost more in sums than they hide, fewer warps hide less (8192 x 512,
-// loss and gradient: 20.1 us; with 8 warps 21.3, and two CTAs a SM 22.0, four
-// 25.3; 64 x 128 in CTAs of 16 warps: 6.5 us instead of 6.2).
+// loss and gradient: 22.3 us; with 8 warps 23.9, two CTAs a SM 25.0, four 25.0;
+// 64 x 128 in CTAs of 16 warps: 6.45 us instead of 6.25).
 constexpr int kBalManyWarps = 16;
 static int balance_clusters(int T, int num_sms) {
   if (T <= 4 * kBalWarps * kBalCluster) return 1;
@@ -410,7 +410,7 @@ static cudaError_t launch_route_backward(const float* logits, long long ld, cons
                                          float* dlogits, long long ldd, int num_sms, cudaStream_t s) {
   const bool vec = E % 4 == 0 && ld % 4 == 0 && ldd % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0 &&
                    (reinterpret_cast<uintptr_t>(dlogits) & 15) == 0;
-  // four CTAs a SM, as many as fit (8192 x 512, loss and gradient: 20.0 us, with two 22.6, with eight in turns 20.9)
+  // four CTAs a SM, as many as fit (8192 x 512, loss and gradient: 22.3 us, with two 24.2, with eight in turns 22.8)
   const int blocks = int(std::min<long long>((T + kBalWarps - 1) / kBalWarps, 4LL * num_sms));
   return balance_variant(E, vec, [&](auto v, auto nv) {
     ProfileScope prof(FT_KERNEL_ROUTE_BACKWARD, s);

@@ -106,8 +106,8 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&v)[16]) 
 // reciprocal and one remainder step (as quotient_by) give the quotient to a step
 // or two of fp32.  A non-finite g follows g / (1 + e^-g): e is 0 or NaN.
 // One h a thread and column stands between a tile's last block and the next
-// tile's first.  The hardware exponential and a fast divide would save 5 us of
-// 278 of the FFN (4096 skewed tokens, 2048 x 768, 128 experts, k = 8), but lose up
+// tile's first.  The hardware exponential and a fast divide would save 6 us of
+// 282 of the FFN (4096 skewed tokens, 2048 x 768, 128 experts, k = 8), but lose up
 // to 2^-18 of h, and all of it where 1 + e^-g passes 2^126.
 __device__ __forceinline__ float fp8_silu_mul(float g, float u) {
   const float e = expf(-fabsf(g)), d = 1.0f + e;
@@ -1176,7 +1176,7 @@ __global__ void __launch_bounds__(256) fp8_prep_kernel(const Fp8PrepParams p) {
 // The rows of x, already quantised once a token, to their places in expert
 // order: a warp a row.  Bound by the writes of k copies.  The kernel above does
 // a token's arithmetic k times instead: at 4096 tokens x 2048, k = 8, the FFN
-// takes 277 us with it and 268 with these two launches (1500 tokens x 2880,
+// takes 295 us with it and 282 with these two launches (1500 tokens x 2880,
 // k = 4: the same within the noise).
 struct Fp8SpreadParams {
   PrepParams sched;
@@ -1371,10 +1371,12 @@ static double fp8_padded(double mean, int b) {
 }
 // Token rows a tile takes (16, 32, 64: the stream kernel; 128, 256: the tile
 // kernel on one CTA or a pair).  For few rows a quarter more than the mean, so
-// that most groups of an even spread are one tile.  A pair takes 0.9 of the
-// time for the same padded rows (32 groups of some 187 rows, two or one tile
-// each: the FFN 249 us against 268) but pads more (4096 skewed tokens of
-// 128 groups: 317 us against 277).
+// that most groups of an even spread are one tile.  A pair takes some 0.9 of the
+// time for the same padded rows, but pads more.  The FFN in pairs and in tiles
+// of 128: groups of some 187 rows, 32 of them 2880 x 2880 253 and 275 us, 128 of
+// them 2048 x 768 216 and 225 to 250; 2048 rows 38 and 40; 250 rows 313 and 311;
+// 256 rows 300 and 270; 125 rows 245 and 214; 75 rows 240 and 169; 4096 skewed
+// tokens of 128 groups 324 and 281.
 static int fp8_rows_tile(double mean) {
   const double rows = 1.25 * mean;
   if (rows <= 64) return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
@@ -1495,8 +1497,8 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
   sp.slot_table = slot_table;
   sp.E = E;
   sp.num_slots = L.num_slots;
-  // The stream kernel finds its tiles itself.  Else a block a unit a thread (4096 skewed tokens of 128 experts, FFN: 274
-  // us, in one block 277).
+  // The stream kernel finds its tiles itself.  Else a block a unit a thread (4096 skewed tokens of 128 experts, FFN: 282
+  // us, in one block 284).
   sp.nsched = stream ? 0 : int(std::min<long long>(32, std::max<long long>(1, (pl.max_units1 + pl.max_units2) / 256)));
   sp.bn1 = sp.bn2 = pl.bn;
   sp.mt1 = pl.mt1;
@@ -1550,9 +1552,9 @@ static cudaError_t launch_fp8_ffn(const void* x, int T, int H, int I, int E, int
     p.E = E;
     p.num_slots = L.num_slots;
     p.early = 1;
-    // While gate/up has a tile a SM at most (128 experts, 2048 x 768, k = 8: one token 17.0 us, apart 20.0; three 31.7
-    // and 34.4); with more, the shorter rings cost more than the early weights give (16 tokens 80.3 and 78.3 us, 64
-    // tokens 115.9 and 110.1).
+    // While gate/up has a tile a SM at most (128 experts, 2048 x 768, k = 8: one token 17.1 us, apart 20.2; three 28.9
+    // and 32.0); with more, the shorter rings cost more than the early weights give (16 tokens 82.8 and 79.6 us, 64
+    // tokens 118.2 and 111.4).
     p.share = pl.bn == 16 && pl.tiles * pl.mt1 <= device_sm_count();
   } else {
     p.units = units1;
