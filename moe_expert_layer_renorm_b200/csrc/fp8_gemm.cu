@@ -153,6 +153,7 @@ struct Fp8StreamCfg {
 };
 // Whatever CTAs of the SHARE kernels shared memory lets on a SM, calls on other streams among them, tensor memory has
 // columns for: no CTA waits in the allocation, where the CTAs of two clusters could hold each other up without a limit.
+// (The other stream kernels fill a SM's shared memory, the tile kernels its registers, which their split needs whole.)
 template <int BN>
 constexpr bool fp8_share_fits() {
   using GateUp = Fp8StreamCfg<2, BN, true>;

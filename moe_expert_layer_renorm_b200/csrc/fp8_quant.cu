@@ -3,8 +3,8 @@
 //   m = max(max |x_i| over the block, 2^-100)     (a NaN is left out)
 //   s = m / 448
 //   q_i = e4m3_rne_sat((448 x_i) / m)             value q_i s
-// The product 448 x_i comes first and is then divided by m, one correctly
-// rounded division: for bf16 and f16 inputs 448 x_i is exact in fp32, so a
+// The product 448 x_i comes first and is then divided by m (quotient_by): for
+// bf16 and f16 inputs 448 x_i is exact in fp32, so a
 // quotient that lies exactly between two codes is seen as the tie it is and
 // goes to the even code (x_i * (448 / m) would round the factor first and
 // push every such tie to one side or the other).  A block whose m is above
